@@ -25,7 +25,8 @@ __all__ = [
     "DfsError", "K", "E", "MAX_L", "lib", "lib_path", "topk", "gate", "pair_scores", "walk",
     "select", "Selector", "select_workspace_bytes", "topk_workspace_bytes", "PackedWeight", "gate_pack",
     "gate_workspace_bytes", "status_str", "conv2", "conv2_workspace_bytes", "Conv2", "lmhead_topk", "lmhead_logits",
-    "lmhead_topk_workspace_bytes",
+    "lmhead_topk_workspace_bytes", "norm_q8", "linear_q8", "linear_q8_workspace_bytes", "tree_attention",
+    "tree_attention_workspace_bytes", "cache_commit",
 ]
 
 K = 16
@@ -50,6 +51,11 @@ class _Shape(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("L", ctypes.c_int64), ("V", ctypes.c_int64),
                 ("d", ctypes.c_int64), ("logits_dtype", ctypes.c_int), ("act_dtype", ctypes.c_int),
                 ("table_dtype", ctypes.c_int)]
+
+
+class _CacheShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "T", "q_heads", "kv_heads", "head_dim", "page_size",
+                                              "n_pages", "table_width")] + [("dtype", ctypes.c_int)]
 
 
 def lib() -> ctypes.CDLL:
@@ -112,6 +118,18 @@ def lib() -> ctypes.CDLL:
         L.dfs_lmhead_topk.restype = c_int
         L.dfs_lmhead_logits.argtypes = [vp, vp, c_int, i64, i64, i64, f32p, vp]
         L.dfs_lmhead_logits.restype = c_int
+        L.dfs_norm_q8.argtypes = [vp, vp, vp, c_int, i64, i64, c_double, vp, f32p, vp, vp, vp]
+        L.dfs_norm_q8.restype = c_int
+        L.dfs_linear_q8_workspace_bytes.argtypes, L.dfs_linear_q8_workspace_bytes.restype = [i64, i64, i64], sz
+        L.dfs_linear_q8.argtypes = [vp, f32p, vp, f32p, i64, i64, i64, c_int, vp, vp, sz, vp]
+        L.dfs_linear_q8.restype = c_int
+        cache = ctypes.POINTER(_CacheShape)
+        L.dfs_tree_attention_workspace_bytes.argtypes = [cache]
+        L.dfs_tree_attention_workspace_bytes.restype = sz
+        L.dfs_tree_attention.argtypes = [vp, vp, vp, i32p, vp, vp, i32p, i32p, cache, c_double, vp, vp, sz, vp]
+        L.dfs_tree_attention.restype = c_int
+        L.dfs_cache_commit.argtypes = [vp, vp, i32p, i32p, i64, vp, vp, i32p, i32p, cache, i32p, vp]
+        L.dfs_cache_commit.restype = c_int
         _lib = L
     return _lib
 
@@ -500,6 +518,196 @@ def lmhead_logits(hidden: torch.Tensor, W_lm: torch.Tensor, out: torch.Tensor | 
     _check(lib().dfs_lmhead_logits(hidden.data_ptr(), W_lm.data_ptr(), BF16, rows, V, d, out.data_ptr(),
                                    _stream(hidden.device)), "dfs_lmhead_logits")
     return out
+
+
+# ---------------------------------------------------------------- verification pass
+
+
+def _same_device(device: torch.device, **tensors) -> None:
+    for what, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{what} must be on {device}, got {t.device}")
+
+
+def _call(device: torch.device, where: str, fn, *args) -> None:
+    """fn(*args, stream) on the tensors' own device and its current stream."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(device)), where)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(device)), where)
+
+
+def _scratch(workspace, device: torch.device, nbytes: int):
+    """The workspace of a call: the caller's, or a new block of the current stream's (a graph's own under capture)."""
+    if nbytes == 0:
+        return None
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _dev(workspace, "workspace")
+    return _ws_arg(workspace, device, nbytes)
+
+
+def norm_q8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+            normed: bool = False, total_out: torch.Tensor | None = None):
+    """Root-mean-square norm of x + residual with an e4m3 output (see dfs_norm_q8).
+
+    x, residual [..., d] and weight [d], all bf16 or all fp32.  Returns (q e4m3 [..., d], scale fp32
+    [ceil(d / 128), rows]), then with a residual the sum in x's dtype (written into ``total_out`` when
+    given, which may be ``x`` or ``residual`` itself), then with ``normed=True`` the norm in x's dtype."""
+    _dev(x, "x")
+    dt = _dtype_code(x, "x")
+    _dev(weight, "weight", x.dtype)
+    if x.dim() < 1 or weight.shape != x.shape[-1:]:
+        raise ValueError("x must be [..., d] and weight [d]")
+    _same_device(x.device, weight=weight, residual=residual, total_out=total_out)
+    if residual is not None:
+        _dev(residual, "residual", x.dtype)
+        if residual.shape != x.shape:
+            raise ValueError("residual must have the shape of x")
+    if total_out is not None:
+        if residual is None:
+            raise ValueError("total_out needs a residual")
+        _dev(total_out, "total_out", x.dtype)
+        if total_out.shape != x.shape:
+            raise ValueError("total_out must have the shape of x")
+    d = x.shape[-1]
+    rows = x.numel() // d if d else 0
+    q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    scale = torch.empty((-(-d // 128), rows), dtype=torch.float32, device=x.device)
+    total = None
+    if residual is not None:
+        total = torch.empty_like(x) if total_out is None else total_out
+    y = torch.empty_like(x) if normed else None
+    _call(x.device, "dfs_norm_q8", lib().dfs_norm_q8, x.data_ptr(), _ptr(residual), weight.data_ptr(), dt, rows, d,
+          float(eps), q.data_ptr(), scale.data_ptr(), _ptr(total), _ptr(y))
+    return (q, scale) + ((total,) if residual is not None else ()) + ((y,) if normed else ())
+
+
+def linear_q8_workspace_bytes(rows: int, N: int, K: int) -> int:
+    return int(lib().dfs_linear_q8_workspace_bytes(rows, N, K))
+
+
+def linear_q8(q: torch.Tensor, scale: torch.Tensor, W: torch.Tensor, W_scale: torch.Tensor,
+              out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The product of e4m3 operands with a scale for each block of 128 (see dfs_linear_q8): [..., N].
+
+    q [..., K] e4m3 with scale [ceil(K / 128), rows] fp32 (``norm_q8``'s); W [N, K] e4m3 with W_scale
+    [ceil(N / 128), ceil(K / 128)] fp32.  ``out_dtype`` bf16 or fp32."""
+    _dev(q, "q", torch.float8_e4m3fn)
+    _dev(scale, "scale", torch.float32)
+    _dev(W, "W", torch.float8_e4m3fn)
+    _dev(W_scale, "W_scale", torch.float32)
+    if q.dim() < 1 or W.dim() != 2 or W.shape[1] != q.shape[-1]:
+        raise ValueError("q must be [..., K] and W [N, K]")
+    N, K = W.shape
+    rows = q.numel() // K if K else 0
+    G = -(-K // 128)
+    if scale.shape != (G, rows) or W_scale.shape != (-(-N // 128), G):
+        raise ValueError(f"scale must be [{G}, {rows}] and W_scale [{-(-N // 128)}, {G}]")
+    if out is None:
+        out = torch.empty(tuple(q.shape[:-1]) + (N,), dtype=out_dtype, device=q.device)
+    else:
+        _dev(out, "out", out_dtype)
+        if out.shape != tuple(q.shape[:-1]) + (N,):
+            raise ValueError("out must be [..., N]")
+    _same_device(q.device, scale=scale, W=W, W_scale=W_scale, out=out)
+    nb = int(lib().dfs_linear_q8_workspace_bytes(rows, N, K))
+    ws = _scratch(workspace, q.device, nb)
+    _call(q.device, "dfs_linear_q8", lib().dfs_linear_q8, q.data_ptr(), scale.data_ptr(), W.data_ptr(),
+          W_scale.data_ptr(), rows, N, K, _dtype_code(out, "out"), out.data_ptr(), _ptr(ws), nb)
+    return out
+
+
+def _cache_args(k_new, v_new, k_pages, v_pages, block_table, lens, q_heads=None) -> _CacheShape:
+    _dev(k_new, "k_new")
+    dt = _dtype_code(k_new, "k_new")
+    _dev(v_new, "v_new", k_new.dtype)
+    _dev(k_pages, "k_pages", k_new.dtype)
+    _dev(v_pages, "v_pages", k_new.dtype)
+    _dev(block_table, "block_table", torch.int32)
+    _dev(lens, "lens", torch.int32)
+    if k_new.dim() != 4 or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must both be [batch, T, kv_heads, head_dim]")
+    batch, T, Hkv, D = k_new.shape
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or k_pages.shape[1] != Hkv or k_pages.shape[3] != D:
+        raise ValueError(f"k_pages and v_pages must both be [n_pages, {Hkv}, page_size, {D}]")
+    if block_table.dim() != 2 or block_table.shape[0] != batch or lens.shape != (batch,):
+        raise ValueError(f"block_table must be [{batch}, width] and lens [{batch}]")
+    _same_device(k_new.device, v_new=v_new, k_pages=k_pages, v_pages=v_pages, block_table=block_table, lens=lens)
+    return _CacheShape(batch, T, Hkv if q_heads is None else q_heads, Hkv, D, k_pages.shape[2], k_pages.shape[0],
+                       block_table.shape[1], dt)
+
+
+def tree_attention_workspace_bytes(batch: int, T: int, q_heads: int, kv_heads: int, head_dim: int, page_size: int,
+                                   n_pages: int, table_width: int) -> int:
+    s = _CacheShape(batch, T, q_heads, kv_heads, head_dim, page_size, n_pages, table_width, BF16)
+    return int(lib().dfs_tree_attention_workspace_bytes(ctypes.byref(s)))
+
+
+def tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, parents: torch.Tensor,
+                   k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor,
+                   scale: float | None = None, out: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of a tree of drafted tokens over a paged cache (see dfs_tree_attention), bf16.
+
+    q [batch, T, q_heads, D]; k_new, v_new [batch, T, kv_heads, D] (the nodes' own keys and values);
+    parents [batch, T] int32 (-1: child of the cache's last token; -2: unused node); k_pages, v_pages
+    [n_pages, kv_heads, page_size, D]; block_table [batch, width] int32; lens [batch] int32.  ``scale``
+    defaults to D ** -0.5.  Returns [batch, T, q_heads, D]."""
+    _dev(q, "q", torch.bfloat16)
+    _dev(parents, "parents", torch.int32)
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, T, q_heads, head_dim]")
+    s = _cache_args(k_new, v_new, k_pages, v_pages, block_table, lens, q.shape[2])
+    if q.dtype != k_new.dtype or q.shape[:2] != k_new.shape[:2] or q.shape[3] != s.head_dim:
+        raise ValueError("q must have k_new's dtype, batch, T and head_dim")
+    if parents.shape != q.shape[:2]:
+        raise ValueError("parents must be [batch, T]")
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _dev(out, "out", q.dtype)
+        if out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+    _same_device(q.device, k_new=k_new, parents=parents, out=out)
+    nb = int(lib().dfs_tree_attention_workspace_bytes(ctypes.byref(s)))
+    ws = _scratch(workspace, q.device, nb)
+    _call(q.device, "dfs_tree_attention", lib().dfs_tree_attention, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+          parents.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
+          ctypes.byref(s), float(s.head_dim ** -0.5 if scale is None else scale), out.data_ptr(), _ptr(ws), nb)
+    return out
+
+
+def cache_commit(k_new: torch.Tensor, v_new: torch.Tensor, nodes: torch.Tensor | None, counts: torch.Tensor,
+                 k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor,
+                 out_lens: torch.Tensor | None = None) -> torch.Tensor:
+    """Puts accepted nodes' keys and values into a paged cache (see dfs_cache_commit), in place.
+
+    k_new, v_new [batch, T, kv_heads, D]; nodes [batch, path_len] int32 (None: node i of a path is i);
+    counts [batch] int32: nodes of the path to take.  Returns the new lengths (``lens`` stays as it is)."""
+    s = _cache_args(k_new, v_new, k_pages, v_pages, block_table, lens)
+    _dev(counts, "counts", torch.int32)
+    if counts.shape != (s.batch,):
+        raise ValueError("counts must be [batch]")
+    path = s.T
+    if nodes is not None:
+        _dev(nodes, "nodes", torch.int32)
+        if nodes.dim() != 2 or nodes.shape[0] != s.batch:
+            raise ValueError("nodes must be [batch, path_len]")
+        path = nodes.shape[1]
+    if out_lens is None:
+        out_lens = torch.empty_like(lens)
+    else:
+        _dev(out_lens, "out_lens", torch.int32)
+        if out_lens.shape != lens.shape:
+            raise ValueError("out_lens must be [batch]")
+    _same_device(k_new.device, nodes=nodes, counts=counts, out_lens=out_lens)
+    _call(k_new.device, "dfs_cache_commit", lib().dfs_cache_commit, k_new.data_ptr(), v_new.data_ptr(), _ptr(nodes),
+          counts.data_ptr(), path, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
+          ctypes.byref(s), out_lens.data_ptr())
+    return out_lens
 
 
 class Selector:

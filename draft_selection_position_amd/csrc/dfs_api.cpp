@@ -24,6 +24,10 @@ inline bool lmhead_shape_ok(int64_t rows, int64_t V, int64_t d) {
   return ((rows + 127) / 128) * ((V + 127) / 128) <= ((int64_t)1 << 23);
 }
 
+// Norm: a row's workgroup of up to 1024 threads, and the launch within 2^31 work-items
+constexpr int64_t kMaxNormD = 65536;
+constexpr int64_t kMaxNormElems = (int64_t)1 << 35;
+
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t pa = (uintptr_t)a, pb = (uintptr_t)b;
@@ -560,6 +564,179 @@ int dfs_lmhead_logits(const void* hidden, const void* W_lm, dfs_dtype_t dt, int6
   if ((st = check_device()) != DFS_OK) return st;
   (void)hipGetLastError();
   return hip_status(launch_lmhead_logits(hidden, W_lm, rows, V, d, out_logits, stream));
+}
+
+int dfs_norm_q8(const void* x, const void* residual, const void* weight, dfs_dtype_t dt, int64_t rows, int64_t d,
+                double eps, uint8_t* out_q, float* out_scale, void* out_total, void* out_norm, hipStream_t stream) {
+  if (!x || !weight || !out_q || !out_scale) return DFS_E_NULL;
+  if (!valid_dtype(dt)) return DFS_E_UNSUPPORTED;
+  if (rows < 1 || rows > DFS_MAX_ROWS || d < 16 || d > kMaxNormD || rows > kMaxNormElems / d) return DFS_E_SHAPE;
+  if (d % 16 != 0) return DFS_E_UNSUPPORTED;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(out_q, 16) ||
+      !aligned(out_scale, 4) || !aligned(out_total, 16) || !aligned(out_norm, 16))
+    return DFS_E_ALIGN;
+  if (!(std::isfinite(eps) && eps >= 0.0) || (out_total && !residual)) return DFS_E_ARG;
+  const size_t n = (size_t)(rows * d) * esize(dt), wn = (size_t)d * esize(dt);
+  const size_t qn = (size_t)(rows * d), sn = (size_t)(rows * cdiv(d, 128)) * 4;
+  struct Span {
+    const void* p;
+    size_t n;
+  };
+  const Span in[3] = {{x, n}, {residual, n}, {weight, wn}};
+  const Span out[4] = {{out_q, qn}, {out_scale, sn}, {out_total, n}, {out_norm, n}};
+  for (int i = 0; i < 4; ++i) {
+    if (!out[i].p) continue;
+    for (const Span& s : in)
+      if (s.p && overlaps(out[i].p, out[i].n, s.p, s.n) &&
+          !(i == 2 && s.p == out_total && s.p != weight))  // the sum may take x's or the residual's place
+        return DFS_E_ARG;
+    for (int j = 0; j < i; ++j)
+      if (out[j].p && overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return DFS_E_ARG;
+  }
+  int st = check_device();
+  if (st != DFS_OK) return st;
+  (void)hipGetLastError();
+  return hip_status(launch_norm_q8(x, residual, weight, dt == DFS_BF16, rows, d, (float)eps, out_q, out_scale,
+                                   out_total, out_norm, stream));
+}
+
+static int check_linear_q8_shape(int64_t rows, int64_t N, int64_t K) {
+  if (rows < 1 || rows > DFS_MAX_ROWS || N < 1 || N > kMaxV || K < 16 || K > kMaxD) return DFS_E_SHAPE;
+  if (cdiv(rows, 64) * cdiv(N, 64) > ((int64_t)1 << 23)) return DFS_E_SHAPE;
+  if (K % 16 != 0) return DFS_E_UNSUPPORTED;
+  return DFS_OK;
+}
+
+size_t dfs_linear_q8_workspace_bytes(int64_t rows, int64_t N, int64_t K) {
+  if (check_linear_q8_shape(rows, N, K) != DFS_OK) return 0;
+  return linear_q8_workspace_bytes(rows, N, K);
+}
+
+int dfs_linear_q8(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale, int64_t rows,
+                  int64_t N, int64_t K, dfs_dtype_t out_dt, void* out, void* ws, size_t ws_bytes,
+                  hipStream_t stream) {
+  if (!a || !a_scale || !w || !w_scale || !out) return DFS_E_NULL;
+  if (!valid_dtype(out_dt)) return DFS_E_UNSUPPORTED;
+  int st = check_linear_q8_shape(rows, N, K);
+  if (st != DFS_OK) return st;
+  if (!aligned(a, 16) || !aligned(a_scale, 4) || !aligned(w, 16) || !aligned(w_scale, 4) || !aligned(out, 16))
+    return DFS_E_ALIGN;
+  const size_t on = (size_t)rows * N * esize(out_dt), G = (size_t)cdiv(K, 128);
+  if (overlaps(out, on, a, (size_t)(rows * K)) || overlaps(out, on, w, (size_t)(N * K)) ||
+      overlaps(out, on, a_scale, G * rows * 4) || overlaps(out, on, w_scale, G * cdiv(N, 128) * 4))
+    return DFS_E_ARG;
+  const size_t need = linear_q8_workspace_bytes(rows, N, K);
+  if (need > 0 && (!ws || ws_bytes < need)) return DFS_E_WORKSPACE;
+  if (ws && !aligned(ws, 256)) return DFS_E_ALIGN;
+  if ((st = check_device()) != DFS_OK) return st;
+  (void)hipGetLastError();
+  return hip_status(launch_linear_q8(a, a_scale, w, w_scale, rows, N, K, out_dt == DFS_BF16, out, ws, stream));
+}
+
+// What the cache's shape must be for either call on it.
+static int check_cache_shape(const dfs_cache_shape_t* s) {
+  if (!s) return DFS_E_NULL;
+  if (!valid_dtype(s->dtype)) return DFS_E_UNSUPPORTED;
+  if (s->batch < 1 || s->batch > 65536 || s->T < 1 || s->T > DFS_MAX_NODES || s->kv_heads < 1 ||
+      s->kv_heads > 1024 || s->batch * s->kv_heads > ((int64_t)1 << 22) || s->head_dim < 8 || s->head_dim > 1024 ||
+      s->page_size < 1 || s->page_size > 65536 || s->n_pages < 1 || s->n_pages > kMaxV || s->table_width < 1 ||
+      s->table_width > ((int64_t)1 << 30) / s->page_size)
+    return DFS_E_SHAPE;
+  if ((s->page_size & (s->page_size - 1)) != 0 || s->head_dim % 8 != 0) return DFS_E_UNSUPPORTED;
+  return DFS_OK;
+}
+
+static int check_attention_shape(const dfs_cache_shape_t* s) {
+  const int st = check_cache_shape(s);
+  if (st != DFS_OK) return st;
+  if (s->q_heads < 1 || s->q_heads > 1024) return DFS_E_SHAPE;
+  if (s->q_heads % s->kv_heads != 0 || (s->head_dim != 64 && s->head_dim != 128) || s->dtype != DFS_BF16)
+    return DFS_E_UNSUPPORTED;
+  return DFS_OK;
+}
+
+static CacheView cache_view(const dfs_cache_shape_t& s, const void* k_pages, const void* v_pages,
+                            const int32_t* block_table, const int32_t* lens) {
+  int shift = 0;
+  while (((int64_t)1 << shift) < s.page_size) ++shift;
+  return CacheView{const_cast<void*>(k_pages), const_cast<void*>(v_pages), block_table, lens, (int)s.n_pages,
+                   (int)s.kv_heads, shift, (int)s.table_width, (int)(s.head_dim * esize(s.dtype))};
+}
+
+// Bytes of the nodes' keys (or values), and of a pool.
+static size_t nodes_bytes(const dfs_cache_shape_t& s) {
+  return (size_t)(s.batch * s.T * s.kv_heads * s.head_dim) * esize(s.dtype);
+}
+static size_t pool_bytes(const dfs_cache_shape_t& s) {
+  return (size_t)s.n_pages * (size_t)(s.kv_heads * s.page_size * s.head_dim) * esize(s.dtype);
+}
+
+size_t dfs_tree_attention_workspace_bytes(const dfs_cache_shape_t* shape) {
+  if (check_attention_shape(shape) != DFS_OK) return 0;
+  const CacheView c = cache_view(*shape, nullptr, nullptr, nullptr, nullptr);
+  return plan_tree_attention(c, shape->batch, shape->T, shape->q_heads / shape->kv_heads, shape->head_dim).ws_bytes;
+}
+
+int dfs_tree_attention(const void* q, const void* k_new, const void* v_new, const int32_t* parents,
+                       const void* k_pages, const void* v_pages, const int32_t* block_table, const int32_t* lens,
+                       const dfs_cache_shape_t* shape, double scale, void* out, void* ws, size_t ws_bytes,
+                       hipStream_t stream) {
+  if (!q || !k_new || !v_new || !parents || !k_pages || !v_pages || !block_table || !lens || !out) return DFS_E_NULL;
+  int st = check_attention_shape(shape);
+  if (st != DFS_OK) return st;
+  const dfs_cache_shape_t s = *shape;
+  if (!aligned(q, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_pages, 16) ||
+      !aligned(v_pages, 16) || !aligned(out, 16) || !aligned(parents, 4) || !aligned(block_table, 4) ||
+      !aligned(lens, 4))
+    return DFS_E_ALIGN;
+  if (!(std::isfinite(scale) && scale > 0.0)) return DFS_E_ARG;
+  const size_t qn = (size_t)(s.batch * s.T * s.q_heads * s.head_dim) * 2, nn = nodes_bytes(s), pn = pool_bytes(s);
+  if (overlaps(out, qn, q, qn) || overlaps(out, qn, k_new, nn) || overlaps(out, qn, v_new, nn) ||
+      overlaps(out, qn, k_pages, pn) || overlaps(out, qn, v_pages, pn) ||
+      overlaps(out, qn, parents, (size_t)(s.batch * s.T) * 4) || overlaps(out, qn, lens, (size_t)s.batch * 4) ||
+      overlaps(out, qn, block_table, (size_t)(s.batch * s.table_width) * 4))
+    return DFS_E_ARG;
+  const CacheView c = cache_view(s, k_pages, v_pages, block_table, lens);
+  const AttnPlan p = plan_tree_attention(c, s.batch, s.T, s.q_heads / s.kv_heads, s.head_dim);
+  if (p.ws_bytes > 0 && (!ws || ws_bytes < p.ws_bytes)) return DFS_E_WORKSPACE;
+  if (ws && !aligned(ws, 256)) return DFS_E_ALIGN;
+  if ((st = check_device()) != DFS_OK) return st;
+  (void)hipGetLastError();
+  return hip_status(launch_tree_attention(p, c, q, k_new, v_new, parents, s.batch, s.T, s.q_heads / s.kv_heads,
+                                          s.head_dim, scale, out, ws, stream));
+}
+
+int dfs_cache_commit(const void* k_new, const void* v_new, const int32_t* nodes, const int32_t* counts,
+                     int64_t path_len, void* k_pages, void* v_pages, const int32_t* block_table,
+                     const int32_t* lens, const dfs_cache_shape_t* shape, int32_t* out_lens, hipStream_t stream) {
+  if (!k_new || !v_new || !counts || !k_pages || !v_pages || !block_table || !lens) return DFS_E_NULL;
+  int st = check_cache_shape(shape);
+  if (st != DFS_OK) return st;
+  const dfs_cache_shape_t s = *shape;
+  if (path_len < 1 || path_len > s.T) return DFS_E_SHAPE;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) ||
+      !aligned(nodes, 4) || !aligned(counts, 4) || !aligned(block_table, 4) || !aligned(lens, 4) ||
+      !aligned(out_lens, 4))
+    return DFS_E_ALIGN;
+  const size_t nn = nodes_bytes(s), pn = pool_bytes(s), bn = (size_t)s.batch * 4;
+  const size_t tn = (size_t)(s.batch * s.table_width) * 4, mn = (size_t)(s.batch * path_len) * 4;
+  struct Span {
+    const void* p;
+    size_t n;
+  };
+  const Span in[6] = {{k_new, nn}, {v_new, nn}, {nodes, mn}, {counts, bn}, {block_table, tn}, {lens, bn}};
+  const Span out[3] = {{k_pages, pn}, {v_pages, pn}, {out_lens, bn}};
+  for (int i = 0; i < 3; ++i) {
+    if (!out[i].p) continue;
+    for (const Span& x : in)
+      if (x.p && overlaps(out[i].p, out[i].n, x.p, x.n)) return DFS_E_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return DFS_E_ARG;
+  }
+  if ((st = check_device()) != DFS_OK) return st;
+  (void)hipGetLastError();
+  return hip_status(launch_cache_commit(cache_view(s, k_pages, v_pages, block_table, lens), k_new, v_new, nodes,
+                                        counts, s.batch, s.T, path_len, out_lens, stream));
 }
 
 }  // extern "C"

@@ -194,4 +194,47 @@ hipError_t launch_lmhead_topk(const void* hidden, const void* W_lm, int64_t rows
 hipError_t launch_lmhead_logits(const void* hidden, const void* W_lm, int64_t rows, int64_t V, int64_t d,
                                 float* out, hipStream_t stream);
 
+// ---------------------------------------------------------------- norm with 8-bit output
+hipError_t launch_norm_q8(const void* x, const void* residual, const void* weight, bool bf16, int64_t rows, int64_t d,
+                          float eps, uint8_t* q, float* scale, void* total, void* normed, hipStream_t stream);
+
+// ---------------------------------------------------------------- 8-bit product
+size_t linear_q8_workspace_bytes(int64_t rows, int64_t N, int64_t K);
+hipError_t launch_linear_q8(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale,
+                            int64_t rows, int64_t N, int64_t K, bool bf16_out, void* out, void* ws,
+                            hipStream_t stream);
+
+// ---------------------------------------------------------------- paged cache
+// Pages [n_pages, kv_heads, page rows, row_bytes] of K and of V, and who owns which.
+struct CacheView {
+  void* k_pages;
+  void* v_pages;
+  const int32_t* block_table;  // [batch, table_width]
+  const int32_t* lens;         // [batch]
+  int n_pages, kv_heads, page_shift, table_width, row_bytes;
+  // a length as the kernels take it: within the table
+  __device__ __forceinline__ int len(int b) const {
+    const int n = lens[b], most = table_width << page_shift;
+    return n < 0 ? 0 : n > most ? most : n;
+  }
+};
+hipError_t launch_cache_commit(const CacheView& c, const void* k_new, const void* v_new, const int32_t* nodes,
+                               const int32_t* counts, int64_t batch, int64_t T, int64_t P, int32_t* out_lens,
+                               hipStream_t stream);
+
+// Workgroups of an attention launch: two for each of MI355X's 256 CUs.
+constexpr int64_t kAttnBlocks = 512;
+struct AttnPlan {
+  int kind;                // waves by key groups x row groups
+  int64_t tile_rows;       // query rows of a workgroup
+  int64_t row_tiles;       // workgroups for a head's rows
+  int64_t G;               // parts that the keys of a head are cut into
+  size_t part_bytes;       // of the parts' fp32 sums; their maxima and sums follow
+  size_t ws_bytes;
+};
+AttnPlan plan_tree_attention(const CacheView& c, int64_t batch, int64_t T, int64_t group, int64_t D);
+hipError_t launch_tree_attention(const AttnPlan& p, const CacheView& c, const void* q, const void* k_new,
+                                 const void* v_new, const int32_t* parents, int64_t batch, int64_t T, int64_t group,
+                                 int64_t D, double scale, void* out, void* ws, hipStream_t stream);
+
 }  // namespace dfs

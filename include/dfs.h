@@ -325,6 +325,106 @@ int dfs_lmhead_topk(const void* hidden, const void* W_lm, dfs_dtype_t dt, int64_
 int dfs_lmhead_logits(const void* hidden, const void* W_lm, dfs_dtype_t dt, int64_t rows, int64_t V,
                       int64_t d, float* out_logits, hipStream_t stream);
 
+/* ---------------------------------------------------------------- 8-bit norm
+ * The target's verification pass over the drafted blocks (the cycle that follows the
+ * selector's path: section "A Lightweight Path Selector" has the target verify the draft)
+ * runs these steps in every layer; dfs_norm_q8 and dfs_linear_q8 are also the way from a
+ * drafter's last hidden state to its logits.
+ *
+ * Root-mean-square norm, after the residual's addition, with an e4m3 (OCP) output and a
+ * scale for each group of 128 columns (the last group of a row may be shorter):
+ *   s = x + residual;  y[c] = s[c] weight[c] / sqrt(mean(s^2) + eps)
+ *   scale[g] = max(max_{c in g} |y[c]| / 448, 2^-100);  q[c] = e4m3(y[c] / scale[g])
+ * all in fp32; s is not rounded before it is normalised, and y / scale is formed as
+ * y (1 / scale), so a value within a few fp32 steps of the border between two e4m3 values
+ * may go to either.  A row whose sum of squares is not finite in fp32 gives NaN throughout;
+ * a NaN or an infinity among a group's y gives it that scale, and NaN for what is not
+ * finite / finite.
+ *   x, residual (NULL: none), weight, out_total, out_norm of dtype dt
+ *   out_q [rows, d] e4m3;  out_scale [ceil(d / 128), rows] fp32 (a group's scales of all
+ *   rows are adjacent, the order in which dfs_linear_q8 takes them)
+ *   out_total [rows, d] = s rounded (NULL: not wanted; needs a residual); it may be x or
+ *   residual itself, and otherwise overlaps neither;  out_norm [rows, d] = y rounded (NULL:
+ *   not wanted)
+ * d a multiple of 16 in [16, 65536], 1 <= rows <= DFS_MAX_ROWS, rows * d <= 2^35; eps finite and
+ * >= 0 (0 with a row of zeros: NaN).  Alignment: out_scale 4 bytes, everything else 16.     */
+int dfs_norm_q8(const void* x, const void* residual, const void* weight, dfs_dtype_t dt, int64_t rows, int64_t d,
+                double eps, uint8_t* out_q, float* out_scale, void* out_total, void* out_norm, hipStream_t stream);
+
+/* ---------------------------------------------------------------- 8-bit product
+ * out[r, n] = sum_g a_scale[g, r] w_scale[n / 128, g] sum_{k in group g} a[r, k] w[n, k]
+ * over groups g of 128 k (the last may be shorter); products and sums in fp32, out rounded
+ * once.  With w an LM head these are the logits that dfs_topk, dfs_select and dfs_verify read.
+ *   a [rows, K], w [N, K] e4m3 (OCP); a_scale [ceil(K / 128), rows] (dfs_norm_q8's order) and
+ *   w_scale [ceil(N / 128), ceil(K / 128)] fp32; out [rows, N] of dtype out_dt, not overlapping an
+ *   input.
+ * K a multiple of 16 in [16, DFS_MAX_D], 1 <= N < 2^31, 1 <= rows <= DFS_MAX_ROWS and
+ * ceil(rows / 64) * ceil(N / 64) <= 2^23.  Alignment: a, w, out 16 bytes; scales 4; ws 256.
+ * ws: dfs_linear_q8_workspace_bytes(rows, N, K) bytes of scratch (may be 0, then ws may be
+ * NULL).                                                                           */
+size_t dfs_linear_q8_workspace_bytes(int64_t rows, int64_t N, int64_t K);
+int dfs_linear_q8(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale, int64_t rows,
+                  int64_t N, int64_t K, dfs_dtype_t out_dt, void* out, void* ws, size_t ws_bytes,
+                  hipStream_t stream);
+
+/* ---------------------------------------------------------------- paged cache
+ * Keys and values of a sequence lie in pages that its row of the block table lists:
+ * position p is row p % page_size of page block_table[b, p / page_size];
+ * k_pages, v_pages [n_pages, kv_heads, page_size, head_dim].                        */
+#define DFS_MAX_NODES 64 /* nodes of a drafted tree */
+typedef struct {
+  int64_t batch;       /* sequences, 1..65536, and batch * kv_heads <= 2^22 */
+  int64_t T;           /* nodes per sequence, 1..DFS_MAX_NODES */
+  int64_t q_heads;     /* query heads, a multiple of kv_heads, <= 1024 */
+  int64_t kv_heads;    /* >= 1; query head h reads kv head h / (q_heads / kv_heads) */
+  int64_t head_dim;    /* 64 or 128 (dfs_cache_commit: a multiple of 8 in [8, 1024]) */
+  int64_t page_size;   /* a power of two, 1..65536 */
+  int64_t n_pages;     /* pages of the pool, 1..2^31-1 */
+  int64_t table_width; /* entries per sequence; table_width * page_size <= 2^30 */
+  dfs_dtype_t dtype;   /* of q, keys, values and the output */
+} dfs_cache_shape_t;
+
+/* ---------------------------------------------------------------- tree attention
+ * Attention of the T nodes of each sequence's drafted tree over the sequence's cache and
+ * the tree itself (a drafted path is the tree whose node t has parent t - 1; T = 1 is plain
+ * decoding of one token).  Node t of sequence b sees the cache's positions 0 .. lens[b] - 1,
+ * itself and its ancestors:
+ *   out[b, t, h] = sum_j softmax_j(scale q[b, t, h] . k_j) v_j
+ *   q, out [batch, T, q_heads, head_dim];  k_new, v_new [batch, T, kv_heads, head_dim]: the
+ *   nodes' own keys and values (they need not be in the cache: dfs_cache_commit puts those of
+ *   accepted tokens there);  parents [batch, T] int32: -1 for a child of the cache's last
+ *   token, else an earlier node.  A node with any other parent is unused: it sees nothing,
+ *   nobody sees it, and its output is zero (as is any row whose weights are all zero).
+ *   lens [batch] int32, clamped to [0, table_width * page_size]; block_table [batch, table_width]
+ *   int32: entries past a sequence's length are not read, and those that are, clamped to the pool.
+ * What is not finite in a key or value that a row does not see does not reach the row.
+ * Scores, maxima, sums and the accumulated output in fp32; softmax weights are rounded to
+ * bf16 for the matrix cores.  dtype must be DFS_BF16; scale finite and > 0.  The order of
+ * sums depends on all lengths of the batch: the same call gives the same bits, the same
+ * sequence in another batch need not.  Alignment: the int32 arrays 4 bytes, everything else 16,
+ * ws 256.  out overlaps no input.
+ * ws: dfs_tree_attention_workspace_bytes(shape) bytes of scratch (may be 0).          */
+size_t dfs_tree_attention_workspace_bytes(const dfs_cache_shape_t* shape);
+int dfs_tree_attention(const void* q, const void* k_new, const void* v_new, const int32_t* parents,
+                       const void* k_pages, const void* v_pages, const int32_t* block_table, const int32_t* lens,
+                       const dfs_cache_shape_t* shape, double scale, void* out, void* ws, size_t ws_bytes,
+                       hipStream_t stream);
+
+/* ---------------------------------------------------------------- cache commit
+ * Accepted tokens into the cache: for i < counts[b] (clamped to [0, path_len]) the key and
+ * value rows of node nodes[b, i] go to position lens[b] + i, and out_lens[b] = lens[b] +
+ * counts[b].  With dfs_verify, a path's counts are out_accepted + 1 where node 0 is the last
+ * verified token.
+ *   k_new, v_new [batch, T, kv_heads, head_dim]; nodes [batch, path_len] int32 (NULL: node i is
+ *   i), 1 <= path_len <= T; counts, lens, out_lens [batch] int32 (out_lens may be NULL and is
+ *   another buffer than lens and counts); shape as for dfs_tree_attention, q_heads not looked at.
+ * The pages that are written must be the sequence's own.  A token whose position lies past the
+ * table, whose page is not one of the pool's or whose node is not in [0, T) is not written.
+ * Alignment: the int32 arrays 4 bytes, the others 16.                               */
+int dfs_cache_commit(const void* k_new, const void* v_new, const int32_t* nodes, const int32_t* counts,
+                     int64_t path_len, void* k_pages, void* v_pages, const int32_t* block_table,
+                     const int32_t* lens, const dfs_cache_shape_t* shape, int32_t* out_lens, hipStream_t stream);
+
 /* Static, NUL-terminated description of a status code; never NULL. */
 const char* dfs_status_str(int status);
 

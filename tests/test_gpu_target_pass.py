@@ -1,0 +1,383 @@
+"""The verification pass's operators on the GPU against the fp64 oracle (oracle/target_pass.py).
+
+Tolerances, from fp32 arithmetic (u = 2^-24 per rounding) and each output's own rounding (half a step,
+eps / 2 of its type):
+  norm     the sum of squares adds at most 64 values per lane, 6 + 16 partial sums: relative error
+           <= 88 u, half of it in its root; three more roundings to y: |y - y*| <= 48 u |y*|.  The scale
+           has one more, the quotient y / scale those of both and three of its own: <= 104 u.  The code is
+           the rounding of some value within that of the exact quotient.
+  product  a block's 128 products are exact in fp32 and each addition in the matrix core is taken to keep
+           2^-23 of the running sum's magnitude; then a multiply-add per block, 8 partial sums where K is
+           split, and the scales' product:  |err| <= (256 + 2 G + 12) u sum |a w| scales.
+  attention  weights rounded to bf16: 2^-8 of sum w |v|.  A score's error (D + 4) u sum |q k| scale and the
+           exponential's argument (rounded once, below 2^7 in size: 2^7 u) change a weight by that much
+           relative, numerator and denominator: twice.  Sums over n keys: 2 n u.  The output: 2^-8.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import target_pass as tp
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+@pytest.fixture(scope="module")
+def dfs():
+    import draft_selection_position_amd as m
+
+    m.lib()
+    return m
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(g, *shape, dtype=torch.float32):
+    return torch.randn(shape, generator=g, device="cuda").to(dtype)
+
+
+# ---------------------------------------------------------------- norm
+
+
+def check_norm(got, x, w, r, eps, normed):
+    y, scale, v, s = tp.norm_q8(f64(x).reshape(-1, x.shape[-1]), f64(w), None if r is None else f64(r).reshape(-1, x.shape[-1]), eps)
+    rel = torch.finfo(x.dtype).eps / 2
+    q, sc = f64(got[0]).reshape(y.shape), f64(got[1])
+    assert got[0].dtype == torch.float8_e4m3fn and sc.shape == scale.shape
+    assert (np.abs(sc - scale) <= 50 * U * scale).all()
+    lo, hi = tp.e4m3_round(v - np.abs(v) * 104 * U), tp.e4m3_round(np.minimum(v + np.abs(v) * 104 * U, 463.0))
+    assert ((q >= np.minimum(lo, hi)) & (q <= np.maximum(lo, hi))).all()
+    i = 2
+    if r is not None:
+        assert (np.abs(f64(got[i]).reshape(s.shape) - s) <= (rel + U) * np.abs(s) + 1e-38).all()
+        i += 1
+    if normed:
+        assert (np.abs(f64(got[i]).reshape(y.shape) - y) <= (rel + 50 * U) * np.abs(y) + 1e-38).all()
+        i += 1
+    assert len(got) == i
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,d", [(1, 16), (3, 128), (1, 512), (2, 528), (17, 1040), (5, 2064), (130, 4112),
+                                    (16, 5120), (2, 8192), (3, 8208), (2, 16400), (1, 33040), (2, 65536)])
+@pytest.mark.parametrize("res,normed", [(True, False), (False, True), (True, True)])
+def test_norm(dfs, dtype, rows, d, res, normed):
+    g = gen(rows * 7 + d)
+    x, w = randn(g, rows, d, dtype=dtype), (1 + 0.3 * randn(g, d)).to(dtype)
+    r = (3 * randn(g, rows, d)).to(dtype) if res else None
+    check_norm(dfs.norm_q8(x, w, r, 1e-5, normed), x, w, r, 1e-5, normed)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norm_many_rows(dfs, dtype):
+    g = gen(5)
+    for rows, d in ((2050, 1024), (4100, 5120), (1500, 336)):
+        x, w, r = randn(g, rows, d, dtype=dtype), randn(g, d, dtype=dtype), randn(g, rows, d, dtype=dtype)
+        check_norm(dfs.norm_q8(x, w, r, 1e-6, True), x, w, r, 1e-6, True)
+
+
+def test_norm_edges(dfs):
+    w = torch.ones(256, device="cuda")
+    x = torch.zeros(4, 256, device="cuda")
+    x[1, 128:] = 2.0  # the other group of the row is zero
+    x[2] = 1e-20      # eps carries the norm: y about 1e-17
+    x[3, 0], x[3, 1:] = 1.0, 1e-30
+    q, s, y = dfs.norm_q8(x, w, eps=1e-6, normed=True)
+    assert (f64(q)[0] == 0).all() and (f64(s)[:, 0] == 2.0 ** -100).all() and f64(s)[0, 1] == 2.0 ** -100
+    check_norm((q, s, y), x, w, None, 1e-6, True)
+    for bad in (float("nan"), float("inf"), 3e38):  # not finite, or its square is not: the row is NaN, the others stay
+        z = torch.ones(3, 256, device="cuda")
+        z[1, 200] = bad
+        q, s, y = dfs.norm_q8(z, w, normed=True)
+        assert np.isnan(f64(q)[1]).all() and np.isnan(f64(s)[:, 1]).all() and np.isnan(f64(y)[1]).all()
+        assert np.isfinite(f64(q)[[0, 2]]).all() and np.isfinite(f64(s)[:, [0, 2]]).all()
+    wn = w.clone()
+    wn[3], wn[200] = float("nan"), float("inf")  # a weight that is not finite: its own group's scale
+    q, s = dfs.norm_q8(torch.ones(2, 256, device="cuda"), wn)
+    assert np.isnan(f64(s)[0]).all() and np.isinf(f64(s)[1]).all()
+    assert np.isnan(f64(q)[:, 200]).all() and (f64(q)[:, 128:200] == 0).all()
+
+
+def test_norm_sum_in_place(dfs):
+    g = gen(9)
+    x, w, r = randn(g, 33, 5120, dtype=torch.bfloat16), randn(g, 5120, dtype=torch.bfloat16), randn(g, 33, 5120, dtype=torch.bfloat16)
+    want = dfs.norm_q8(x, w, r)
+    for name in ("x", "r"):
+        a = {"x": x.clone(), "r": r.clone()}
+        got = dfs.norm_q8(a["x"], w, a["r"], total_out=a[name])
+        assert got[2].data_ptr() == a[name].data_ptr()
+        for p, q in zip(got, want):
+            assert torch.equal(p.view(torch.uint8), q.view(torch.uint8))
+
+
+# ---------------------------------------------------------------- product
+
+
+def quantised(g, n, K, rows, std=1.0):
+    x = std * randn(g, n, K)
+    G, R = -(-K // 128), -(-n // rows)
+    p = torch.nn.functional.pad(x, (0, G * 128 - K, 0, R * rows - n)).view(R, rows, G, 128)
+    s = (p.abs().amax(dim=(1, 3)) / 448).clamp_min(2.0 ** -100)
+    q = (p / s[:, None, :, None]).view(R * rows, G * 128)[:n, :K].to(torch.float8_e4m3fn).contiguous()
+    return q, s.contiguous()
+
+
+def check_linear(dfs, g, rows, N, K, dtype):
+    a, sa = quantised(g, rows, K, 1)
+    sa = sa.t().contiguous()
+    w, sw = quantised(g, N, K, 128, 0.05)
+    out = dfs.linear_q8(a, sa, w, sw, out_dtype=dtype)
+    want, mag = tp.linear_q8(f64(a), f64(sa), f64(w), f64(sw))
+    tol = (256 + 2 * -(-K // 128) + 12) * U * mag + torch.finfo(dtype).eps / 2 * np.abs(want) + 1e-38
+    err = np.abs(f64(out) - want)
+    assert out.shape == (rows, N) and out.dtype == dtype
+    far = (err / tol).max()
+    assert far <= 1, far
+    print(f"rows {rows} N {N} K {K} {dtype}: largest error / bound {(err / tol).max():.3f}", flush=True)
+
+
+LINEAR = [(1, 1, 16), (1, 16, 128), (2, 130, 144), (16, 1000, 256), (17, 257, 400), (16, 5003, 2064), (33, 520, 1024),
+          (48, 2000, 512), (64, 129, 2176), (65, 300, 640), (100, 5003, 272), (128, 128, 128), (129, 1027, 1040),
+          (256, 256, 256), (333, 515, 2064), (513, 1030, 384), (1, 5120, 4096), (7, 30000, 528)]
+
+
+@pytest.mark.parametrize("rows,N,K", LINEAR)
+def test_linear(dfs, rows, N, K):
+    for dtype in (torch.float32, torch.bfloat16):
+        check_linear(dfs, gen(rows + N + K), rows, N, K, dtype)
+
+
+@pytest.mark.parametrize("rows,N,K", [(700, 9001, 1040), (2049, 2600, 768), (1024, 5120, 1024), (4096, 1000, 336)])
+def test_linear_many_rows(dfs, rows, N, K):
+    check_linear(dfs, gen(N), rows, N, K, torch.bfloat16)
+    check_linear(dfs, gen(N + 1), rows, N, K, torch.float32)
+
+
+def test_linear_values_that_are_not_finite(dfs):
+    """A NaN or an infinite scale reaches its own row or column only (the matrix core reads whole tiles)."""
+    g = gen(3)
+    for rows, N, K in ((5, 300, 272), (150, 300, 272)):
+        a, sa = quantised(g, rows, K, 1)
+        sa = sa.t().contiguous()
+        w, sw = quantised(g, N, K, 128)
+        clean = f64(dfs.linear_q8(a, sa, w, sw, out_dtype=torch.float32))
+        a2, w2, sa2 = a.clone(), w.clone(), sa.clone()
+        a2.view(torch.uint8)[1, 270] = 0x7F
+        w2.view(torch.uint8)[299, 0] = 0xFF
+        sa2[2, 3] = float("inf")
+        got = f64(dfs.linear_q8(a2, sa2, w2, sw, out_dtype=torch.float32))
+        assert np.isnan(got[1]).all() and np.isnan(got[:, 299]).all() and not np.isfinite(got[3]).any()
+        keep = np.ones((rows, N), bool)
+        keep[1], keep[:, 299], keep[3] = False, False, False
+        np.testing.assert_array_equal(got[keep], clean[keep])
+
+
+def test_linear_exact_sums(dfs):
+    """Small whole numbers with scales that are powers of two: the sums are exact in fp32, and so is the result."""
+    g = gen(11)
+    for rows, N, K in ((3, 200, 384), (40, 200, 384), (140, 1000, 384), (600, 1000, 384)):
+        a = torch.randint(-8, 9, (rows, K), generator=g, device="cuda").float().to(torch.float8_e4m3fn)
+        w = torch.randint(-8, 9, (N, K), generator=g, device="cuda").float().to(torch.float8_e4m3fn)
+        sa = 2.0 ** torch.randint(-2, 3, (3, rows), generator=g, device="cuda").float()
+        sw = 2.0 ** torch.randint(-2, 3, (-(-N // 128), 3), generator=g, device="cuda").float()
+        want, _ = tp.linear_q8(f64(a), f64(sa), f64(w), f64(sw))
+        np.testing.assert_array_equal(f64(dfs.linear_q8(a, sa, w, sw, out_dtype=torch.float32)), want)
+
+
+# ---------------------------------------------------------------- attention and cache
+
+
+def cache(g, lens, Hkv, D, page, spare=0, dtype=torch.bfloat16, fill=None):
+    """Shuffled pages with room for lens + spare tokens; the table's entries behind them point nowhere."""
+    need = [max(0, -(-(n + spare) // page)) for n in lens]
+    total = sum(need) + 2
+    order = torch.randperm(total, generator=g, device="cuda").to(torch.int32)
+    table = torch.full((len(lens), max(1, max(need)) + 1), -(1 << 30), dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    pools = [randn(g, total, Hkv, page, D, dtype=dtype) for _ in range(2)]
+    if fill is not None:  # whatever no sequence owns
+        for p in pools:
+            own = torch.zeros(total, page, dtype=torch.bool, device="cuda")
+            for b, n in enumerate(lens):
+                pos = torch.arange(n, device="cuda")
+                own[table[b, pos // page].long(), pos % page] = True
+            p.transpose(1, 2)[~own] = fill
+    return pools[0], pools[1], table, torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+def trees(g, B, T, kind):
+    node = torch.arange(T, device="cuda")
+    if kind == "chain":
+        return (node - 1).expand(B, T).to(torch.int32).contiguous()
+    p = (torch.rand(B, T, generator=g, device="cuda") * (node + 1)).floor().long() - 1
+    if kind == "holes":
+        p = torch.where(torch.rand(B, T, generator=g, device="cuda") < 0.25, torch.where(node % 2 == 0, -2, node + 1), p)
+    return p.to(torch.int32).contiguous()
+
+
+def check_attention(dfs, q, kn, vn, par, kp, vp, table, lens, scale=None, got=None):
+    out = dfs.tree_attention(q, kn, vn, par, kp, vp, table, lens, scale) if got is None else got
+    sc = q.shape[-1] ** -0.5 if scale is None else scale
+    want, mag, dots, keys = tp.tree_attention(f64(q), f64(kn), f64(vn), par.tolist(), f64(kp), f64(vp),
+                                              table.cpu().numpy(), lens.tolist(), sc)
+    D = q.shape[-1]
+    tol = mag * (2.0 ** -8 + 2 * ((D + 4) * U * dots + 2.0 ** 7 * U) + 2 * keys * U)[..., None] + 2.0 ** -8 * np.abs(want) + 1e-30
+    err = np.abs(f64(out) - want)
+    far = (err / tol).max()
+    assert far <= 1, (np.unravel_index((err / tol).argmax(), err.shape), far)
+    print(f"largest error / bound {(err / tol).max():.3f}", flush=True)
+
+
+def make(seed, lens, T, Hkv, group, D, page, kind="chain", fill=None, qstd=1.5):
+    g = gen(seed)
+    B = len(lens)
+    kp, vp, table, ln = cache(g, lens, Hkv, D, page, fill=fill)
+    return [randn(g, B, T, Hkv * group, D).mul(qstd).bfloat16(), randn(g, B, T, Hkv, D, dtype=torch.bfloat16),
+            randn(g, B, T, Hkv, D, dtype=torch.bfloat16), trees(g, B, T, kind), kp, vp, table, ln]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,T,Hkv,group,page,kind", [
+    ([0], 1, 1, 1, 1, "chain"),              # nothing but the node itself
+    ([1], 1, 2, 1, 16, "chain"),
+    ([0, 5, 64, 63, 65], 1, 2, 4, 16, "chain"),
+    ([127, 128, 129, 0], 3, 1, 8, 32, "random"),
+    ([200, 1], 16, 2, 4, 1, "random"),       # 64 rows
+    ([130, 300], 17, 2, 4, 64, "chain"),     # 68 rows
+    ([33, 700], 32, 1, 3, 16, "holes"),      # 96 rows
+    ([100, 64, 1000], 64, 2, 2, 128, "random"),
+    ([513], 64, 1, 7, 16, "holes"),          # 448 rows
+    ([2000], 1, 3, 5, 16, "chain"),
+    ([40] * 70, 2, 1, 2, 16, "random"),      # more sequences than a wave has lanes
+])
+def test_attention(dfs, D, lens, T, Hkv, group, page, kind):
+    check_attention(dfs, *make(len(lens) + T, lens, T, Hkv, group, D, page, kind))
+
+
+def test_attention_long_and_even_split(dfs):
+    check_attention(dfs, *make(1, [9001, 3], 5, 1, 4, 128, 256, "random"))
+    check_attention(dfs, *make(2, [6000], 33, 2, 2, 64, 64, "random"))
+
+
+def test_attention_many_sequences(dfs):
+    lens = [(37 * b) % 50 for b in range(600)]
+    check_attention(dfs, *make(3, lens, 2, 1, 2, 64, 16, "chain"))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,group", [(5, 2), (20, 3), (33, 4)])
+def test_attention_ignores_what_is_not_seen(dfs, D, T, group):
+    """NaN and infinities in the pages' other rows, in unused nodes and in nodes of other branches."""
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        a = make(7, [70, 0, 129], T, 2, group, D, 16, "holes")
+        b = make(7, [70, 0, 129], T, 2, group, D, 16, "holes", fill=bad)
+        want = dfs.tree_attention(*a)
+        par = a[3].tolist()
+        sees = [tp.ancestors(p) for p in par]
+        kill = torch.tensor([[s is None for s in q] for q in sees], device="cuda")
+        leaf = [next(t for t in reversed(range(T)) if sees[i][t] is not None) for i in range(3)]
+        for t in (1, 2):
+            b[t][kill] = bad
+            for i, n in enumerate(leaf):
+                b[t][i, n] = bad
+        got = dfs.tree_attention(*b)
+        hit = torch.zeros(3, T, dtype=torch.bool, device="cuda")
+        for i, n in enumerate(leaf):
+            hit[i, n] = True
+        assert torch.equal(got[~hit].view(torch.int16), want[~hit].view(torch.int16))
+        assert not torch.isfinite(got[hit].float()).any()
+        assert (got[kill] == 0).all()
+
+
+def test_attention_infinite_values(dfs):
+    """An infinite V of the last position and of a node: infinite where it is seen, the sign kept."""
+    for T, group in ((3, 2), (40, 2)):
+        a = make(8, [37], T, 1, group, 64, 16, "chain")
+        page, row = int(a[6][0, 36 // 16]), 36 % 16
+        a[5][page, 0, row, 5] = float("inf")
+        a[2][0, 1, 0, 9] = -float("inf")
+        out = dfs.tree_attention(*a).float()
+        assert (out[..., 5] == float("inf")).all()
+        assert (out[0, 1:, :, 9] == -float("inf")).all() and torch.isfinite(out[0, 0, :, 9]).all()
+        rest = [i for i in range(64) if i not in (5, 9)]
+        assert torch.isfinite(out[..., rest]).all()
+
+
+def test_attention_large_scores(dfs):
+    """Scores of some thousands: one key has all the weight; growing and shrinking along the sequence."""
+    for sign in (1, -1):
+        a = make(9, [400, 130], 6, 2, 2, 64, 16, "random", qstd=1.0)
+        ramp = torch.arange(400, device="cuda").float() * sign
+        pos = torch.arange(400, device="cuda")
+        a[4][a[6][0, pos // 16].long(), :, pos % 16] = (ramp[:, None, None] / 8 + torch.zeros(400, 2, 64, device="cuda")).bfloat16()
+        a[0][:] = 1.0
+        check_attention(dfs, *a)
+
+
+def test_attention_lengths_and_pages_out_of_range(dfs):
+    a = make(10, [40, 64], 3, 2, 2, 64, 16)
+    want = dfs.tree_attention(*a)
+    a[7][0] = -5  # as an empty cache
+    got = dfs.tree_attention(*a)
+    assert torch.equal(got[1], want[1])
+    a[7][0] = 0
+    assert torch.equal(dfs.tree_attention(*a)[0], got[0])
+    a[7][1] = 1 << 30  # as far as the table goes; its last entry is clamped into the pool
+    assert torch.isfinite(dfs.tree_attention(*a).float()).all()
+
+
+def test_attention_scale_and_out(dfs):
+    a = make(11, [50], 4, 1, 2, 128, 32)
+    out = torch.full((2, 4, 2, 128), 7.0, device="cuda", dtype=torch.bfloat16)
+    got = dfs.tree_attention(*a, scale=0.3, out=out[:1])
+    check_attention(dfs, *a, scale=0.3, got=got)
+    assert (out[1] == 7).all()
+
+
+@pytest.mark.parametrize("dtype,D", [(torch.bfloat16, 128), (torch.bfloat16, 8), (torch.float32, 64), (torch.float32, 72)])
+@pytest.mark.parametrize("page", [1, 16, 64])
+def test_commit(dfs, dtype, D, page):
+    g = gen(D + page)
+    lens, T, Hkv, P = [0, 5, 63, 64, 17], 9, 3, 6
+    kp, vp, table, ln = cache(g, lens, Hkv, D, page, spare=P, dtype=dtype)
+    kn, vn = randn(g, 5, T, Hkv, D, dtype=dtype), randn(g, 5, T, Hkv, D, dtype=dtype)
+    for nodes in (None, torch.randint(0, T, (5, P), generator=g, device="cuda").to(torch.int32)):
+        counts = torch.tensor([0, 6, 1, 3, 99 if nodes is not None else 2], dtype=torch.int32, device="cuda")
+        k2, v2 = kp.clone(), vp.clone()
+        got = dfs.cache_commit(kn, vn, nodes, counts, k2, v2, table, ln)
+        wk, wv, wl = tp.cache_commit(f64(kn), f64(vn), None if nodes is None else nodes.cpu().numpy(), counts.tolist(),
+                                     f64(kp), f64(vp), table.cpu().numpy(), lens)
+        np.testing.assert_array_equal(f64(k2), wk)
+        np.testing.assert_array_equal(f64(v2), wv)
+        assert got.tolist() == wl.tolist() and ln.tolist() == lens
+
+
+def test_commit_skips_what_does_not_fit(dfs):
+    g = gen(1)
+    kp, vp, table, ln = cache(g, [14, 15], 2, 64, 16)
+    table = table[:, :1].contiguous()  # one page each
+    kn, vn = randn(g, 2, 4, 2, 64, dtype=torch.bfloat16), randn(g, 2, 4, 2, 64, dtype=torch.bfloat16)
+    nodes = torch.tensor([[0, 1, 2, 3], [7, 0, 1, -1]], dtype=torch.int32, device="cuda")
+    counts = torch.tensor([4, 2], dtype=torch.int32, device="cuda")
+    k2, v2 = kp.clone(), vp.clone()
+    lens = dfs.cache_commit(kn, vn, nodes, counts, k2, v2, table, ln)
+    wk, wv, wl = tp.cache_commit(f64(kn), f64(vn), nodes.cpu().numpy(), [4, 2], f64(kp), f64(vp), table.cpu().numpy(), [14, 15])
+    np.testing.assert_array_equal(f64(k2), wk)
+    np.testing.assert_array_equal(f64(v2), wv)
+    assert lens.tolist() == [18, 17]
