@@ -28,6 +28,12 @@ COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-Wno-unused-result",
           f"-I{os.path.join(ROOT, 'include')}"]
 
 
+# Of single sources.  attention.hip: matrix products with their sums in ordinary registers; where
+# only one wave fits a SIMD the compiler would keep them in accumulation registers and copy
+# them back and forth (750 copies in the kernel for few rows).
+SOURCE_FLAGS = {"attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+
+
 def hipcc() -> str:
     for cand in (os.environ.get("HIPCC"), "/opt/rocm/bin/hipcc", shutil.which("hipcc")):
         if cand and os.path.exists(cand):
@@ -45,7 +51,7 @@ HOST_SANITIZE = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize
 
 def _compile(src: str, out_dir: str = BUILD, extra=()) -> str:
     obj = os.path.join(out_dir, os.path.basename(src) + ".o")
-    cmd = [hipcc(), f"--offload-arch={ARCH}", *COMMON, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [hipcc(), f"--offload-arch={ARCH}", *COMMON, *SOURCE_FLAGS.get(src, []), *extra, "-c", os.path.join(CSRC, src), "-o", obj]
     if src.endswith(".hip"):
         cmd.insert(1, "-x")
         cmd.insert(2, "hip")

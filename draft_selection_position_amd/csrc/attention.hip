@@ -14,12 +14,14 @@
 // to bf16 for the matrix cores (relative 2^-9 per weight, as the output's own rounding);
 // scores, maxima, sums and O stay in fp32.
 //
-// K and V tiles go from memory straight into LDS, two stages: one lands while the other is
-// computed.  Waves of a workgroup: RW row groups of 32 rows share a key tile, KW key groups
-// take tiles of their own (few rows) and are joined at the end.  Work is split along the
-// keys: the tiles of all sequences in a row are cut evenly over the workgroups of a head,
-// whatever the lengths are; sequences that were cut are joined by a second kernel from
-// fp32 partial results.
+// K and V tiles of 32 keys go from memory straight into LDS, through a ring of stages.  Few
+// query rows: four waves take tiles of their own and never wait for each other until they
+// are joined at the end.  More rows: the waves of a workgroup share a tile, 32 rows each.
+// Pages are looked up two ring lengths ahead, through LDS as well: a load into a register
+// in the loop would make the compiler wait for everything in flight.  Work is split along
+// the keys: the tiles of all sequences in a row are cut evenly over the workgroups of a
+// head, whatever the lengths are; sequences that were cut are joined by a second kernel
+// from fp32 partial results.
 #include "dfs_device.h"
 #include "dfs_internal.h"
 #include "mfma_big.h"
@@ -34,7 +36,6 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kMaxNodes = 64;
 constexpr float kLag = 8.0f;  // a maximum may lag this far (in powers of two) before sums are rescaled
 
 struct AttnArgs {
@@ -47,29 +48,59 @@ struct AttnArgs {
   float* part_o;   // [Hkv, row tiles, 2 G, rows of a tile, D]
   float* part_ml;  // [Hkv, row tiles, 2 G, rows of a tile, 2]
   int batch, T, group, G, row_tiles;
+  bool many;  // parts a sequence is cut into: eight or more, as a rule
   float c2;  // scale * log2(e)
 };
 
-template <int D_, int KW_, int RW_, int TK_>
+// KW key groups x RW row groups of waves, a ring of S stages of 32 SUB keys.
+template <int D_, int KW_, int RW_, int S_, int SUB_ = 1>
 struct Cfg {
-  static constexpr int D = D_, KW = KW_, RW = RW_, TK = TK_;
+  static constexpr int D = D_, KW = KW_, RW = RW_, S = S_;
+  static_assert(KW == 1 || RW == 1, "waves share a tile, or have their own");
   static constexpr int kWaves = KW * RW, kThreads = 64 * kWaves;
+  static constexpr bool kOnce = RW < 4;  // one workgroup has all rows of a head
   static constexpr int kRows = 32 * RW;            // query rows of a workgroup
-  static constexpr int kTile = KW * TK;            // keys per step
+  static constexpr int SUB = SUB_, kKeys = 32 * SUB;  // keys of a group's step
+  static constexpr int kTile = KW * kKeys;         // of a workgroup's
   static constexpr int kRowBytes = 2 * D;          // of a key in LDS
   static constexpr int kChunks = kRowBytes / 16;   // 16-byte chunks
   static constexpr int kRowsPerLoad = 64 / kChunks;
-  static constexpr int kHalf = TK * kRowBytes;     // K (or V) of a key group's step
-  static constexpr int kLoadsAll = 2 * TK / kRowsPerLoad;              // of a key group per step
-  static constexpr int kLoads = (kLoadsAll + RW - 1) / RW;             // of a wave (some repeated when uneven)
-  static constexpr int kStage = KW * 2 * kHalf;
-  static constexpr int kLds = 2 * kStage;
-  static constexpr int kMinWaves = kLds > 81920 ? 1 : 2;  // per SIMD: one workgroup of a CU, or two
+  static constexpr int kHalf = kKeys * kRowBytes;  // K (or V) of a group's step
+  static constexpr int kLoadsAll = kKeys / kRowsPerLoad;    // loads of them
+  static constexpr int kLoads = (kLoadsAll + RW - 1) / RW;  // of a wave (some repeated when uneven)
+  static constexpr int kInFlight = (S - 2) * 2 * kLoads;    // loads of the steps after the one that is waited for
+  static constexpr int kStage = 2 * kHalf;         // of a key group
+  static constexpr int kAhead = 2 * (S - 1);       // steps that pages are looked up ahead
+  static constexpr int kPages = 256;               // bytes of a wave's pages of one step
+  static constexpr int kRing = KW * S * kStage;
+  static constexpr int kJoin = KW > 1 ? (KW - 1) * (D / 2 + 2) * 256 : 0;  // key groups meet in the ring's LDS
+  static_assert(kJoin <= kRing, "LDS of the join");
+  static constexpr int kLds = kRing + kWaves * (kAhead + 1) * kPages;
+  static constexpr int kMost = D == 64 ? 3 : 2;  // waves that a SIMD's registers hold
+  static constexpr int kByLds = 163840 / (kLds + 2304), kByWaves = 4 * kMost / kWaves;
+  static constexpr int kGroups = kByLds < kByWaves ? kByLds : kByWaves;  // workgroups of a CU
+  static constexpr int kMinWaves = kGroups * kWaves > 8 ? 3 : kGroups * kWaves > 4 ? 2 : 1;  // per SIMD
 };
 
-// 16 bytes per lane from memory straight into LDS at lds_base + 16 lane.
+// 16 bytes per lane from memory straight into LDS at lds_base + 16 lane; kOnce: nobody else
+// reads them (64 sequences x 17 nodes, 8192 keys: 232 us against 254 without the hint).
+template <bool kOnce>
 __device__ __forceinline__ void dma16(const void* p, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(p), "s"(lds_base) : "memory", "m0");
+  if constexpr (kOnce)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt"
+                 :
+                 : "v"(p), "s"(lds_base)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                 :
+                 : "v"(p), "s"(lds_base)
+                 : "memory", "m0");
+}
+
+// 4 bytes per lane, at lds_base + 4 lane.
+__device__ __forceinline__ void dma4(const void* p, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(p), "s"(lds_base) : "memory", "m0");
 }
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
@@ -91,42 +122,75 @@ __device__ __forceinline__ float xor32(float x, int lane) {
   return __uint_as_float(xor_lanes(__float_as_uint(x), 32, lane));
 }
 
+__device__ __forceinline__ uint64_t shfl64(uint64_t x, int src) {
+  return ((uint64_t)(uint32_t)__shfl((uint32_t)(x >> 32), src) << 32) | (uint32_t)__shfl((uint32_t)x, src);
+}
+
 // Tiles of a sequence: its cache's, and the tree's.
-__device__ __forceinline__ int seq_tiles(int len, int tile) { return (len + tile - 1) / tile + 1; }
+template <class C>
+__device__ __forceinline__ int cache_tiles(int len) {
+  return (len + C::kTile - 1) / C::kTile;
+}
+template <class C>
+__device__ __forceinline__ int seq_tiles(const AttnArgs& a, int b) {
+  return cache_tiles<C>(a.c.len(b)) + (a.T + C::kTile - 1) / C::kTile;
+}
+
+// a b / c rounded down, for a b < 2^53 and c < 2^32: the quotient is at least 1 / c away from
+// the next whole number above it, far more than its rounding in 64 bits.
+__device__ __forceinline__ int mul_div(int a, int b, int c) { return (int)((double)a * (double)b / (double)c); }
 
 // Total tiles, and the sequence that holds tile `want(total)` with the tiles before it.
 struct Where {
-  int64_t total, before;
-  int seq;
+  int total, before, seq;
 };
-template <int kThreads, class F>
-__device__ __forceinline__ Where locate(const AttnArgs& a, int tile, int64_t* scratch, F want) {
-  // each thread a run of sequences; scratch: kThreads + 2 values of LDS
+// Up to 64 sequences: a lane each, every wave by itself.
+template <class C, class F>
+__device__ __forceinline__ Where locate_wave(const AttnArgs& a, int lane, F want) {
+  const int mine = lane < a.batch ? seq_tiles<C>(a, lane) : 0;
+  int upto = mine;  // tiles of the sequences up to this lane's
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl(upto, max(lane - d, 0));
+    if (lane >= d) upto += v;
+  }
+  Where w;
+  w.total = __builtin_amdgcn_readlane(upto, 63);
+  const int x = want(w.total);
+  w.seq = __popcll(__ballot(lane < a.batch && upto <= x));
+  w.before = __builtin_amdgcn_readlane(upto - mine, w.seq);
+  return w;
+}
+// More: a run of sequences per thread; scratch: kThreads + 2 values of LDS.
+template <class C, class F>
+__device__ __forceinline__ Where locate(const AttnArgs& a, int* scratch, F want) {
+  if (a.batch == 1) return Where{seq_tiles<C>(a, 0), 0, 0};
+  if (a.batch <= 64) return locate_wave<C>(a, threadIdx.x & 63, want);
+  constexpr int kThreads = C::kThreads;
   const int per = (a.batch + kThreads - 1) / kThreads;
   const int lo = threadIdx.x * per, hi = min(lo + per, a.batch);
-  int64_t mine = 0;
-  for (int b = lo; b < hi; ++b) mine += seq_tiles(a.c.len(b), tile);
+  int mine = 0;
+#pragma unroll 1
+  for (int b = lo; b < hi; ++b) mine += seq_tiles<C>(a, b);
   scratch[threadIdx.x] = mine;
   __syncthreads();
-  int64_t before = 0, total = 0;
-  const int active = min(kThreads, (a.batch + per - 1) / per);
-  for (int i = 0; i < active; ++i) {
-    const int64_t v = scratch[i];
+  int before = 0, total = 0;
+#pragma unroll 8
+  for (int i = 0; i < kThreads; ++i) {
+    const int v = scratch[i];
     if (i < (int)threadIdx.x) before += v;
     total += v;
   }
-  const int64_t x = want(total);
+  const int x = want(total);
   if (x >= before && x < before + mine) {
-    int b = lo;
-    int64_t at = before;
-    for (int n; x >= at + (n = seq_tiles(a.c.len(b), tile)); ++b) at += n;
+    int b = lo, at = before;
+#pragma unroll 1
+    for (int n; x >= at + (n = seq_tiles<C>(a, b)); ++b) at += n;
     scratch[kThreads] = at;
     scratch[kThreads + 1] = b;
   }
   __syncthreads();
-  Where w{total, scratch[kThreads], (int)scratch[kThreads + 1]};
-  __syncthreads();
-  return w;
+  return Where{total, scratch[kThreads], scratch[kThreads + 1]};
 }
 
 // The nodes that node `lane` sees, as bits (none for an unused node): itself and, by
@@ -136,8 +200,8 @@ __device__ __forceinline__ uint64_t tree_bits(const int32_t* parents, int T, int
   const bool used = p >= -1 && p < lane;
   uint64_t bits = used ? 1ull << lane : 0;
   if (!used) p = -1;
-#pragma unroll
-  for (int i = 0; i < 6; ++i) {
+#pragma unroll 1
+  for (int reach = 1; reach < T; reach *= 2) {
     const int src = p < 0 ? lane : p;
     const uint32_t lo = __shfl((uint32_t)bits, src), hi = __shfl((uint32_t)(bits >> 32), src);
     const int pp = __shfl(p, src);
@@ -149,32 +213,11 @@ __device__ __forceinline__ uint64_t tree_bits(const int32_t* parents, int T, int
   return bits;
 }
 
-__device__ __forceinline__ uint64_t shfl64(uint64_t x, int src) {
-  return ((uint64_t)(uint32_t)__shfl((uint32_t)(x >> 32), src) << 32) | (uint32_t)__shfl((uint32_t)x, src);
-}
-
 template <class C>
 struct State {
   f32x16 o[C::D / 32];  // o[dt][i]: d = 32 dt + 8 (i / 4) + 4 half + i % 4 of this lane's row
   float m, l;           // maximum (in powers of two; -inf: nothing seen) and sum
 };
-
-// Loads of one step into `stage`: this wave's share of its key group's K and V rows.
-// row_of(key of the tile) gives the row's K address; V lies `v_off` bytes after it.
-template <class C, class F>
-__device__ __forceinline__ void load_tile(char* group, int rw, int lane, F row_of) {
-  const int rr = lane / C::kChunks, slot = lane % C::kChunks;
-#pragma unroll
-  for (int i = 0; i < C::kLoads; ++i) {
-    int j = rw + C::RW * i;
-    if (C::kLoadsAll % C::RW != 0) j = min(j, C::kLoadsAll - 1);
-    const bool isv = j >= C::kLoadsAll / 2;
-    const int row = (isv ? j - C::kLoadsAll / 2 : j) * C::kRowsPerLoad + rr;
-    const int chunk = isv ? v_slot<C>(slot, row) : k_slot<C>(slot, row);
-    const char* p = row_of(row, isv) + 16 * chunk;
-    dma16(p, __builtin_amdgcn_readfirstlane(lds_addr(group + j * 1024)));
-  }
-}
 
 // Clears the V rows of keys that are not `there`: a weight of zero must not meet what is
 // not finite in them.  With `others` also what is not finite in the rows that are; says
@@ -183,7 +226,7 @@ template <class C>
 __device__ __forceinline__ bool clear_rows(char* vt, int rw, int lane, uint64_t there, bool others) {
   bool odd = false;
 #pragma unroll 1
-  for (int u = rw * 64 + lane; u < C::TK * C::kChunks; u += 64 * C::RW) {
+  for (int u = rw * 64 + lane; u < C::kKeys * C::kChunks; u += 64 * C::RW) {
     const int row = u / C::kChunks;
     uint4* at = reinterpret_cast<uint4*>(vt + row * C::kRowBytes + 16 * (u % C::kChunks));
     if (!((there >> row) & 1)) {
@@ -220,180 +263,250 @@ struct Frag {
   }
 };
 
-// A step's TK keys: scores, weights, sums.  `masked`: only the keys whose bit is set in
+// A step's 32 keys: scores, weights, sums.  `masked`: only the keys whose bit is set in
 // this lane's `sees` count.
 template <class C>
 __device__ __forceinline__ void step(lds_t kt, lds_t vt, const Frag<C>& at, const bf16x8 (&qf)[C::D / 16], float c2,
-                                     int lane, bool masked, uint64_t sees, State<C>& st) {
+                                     int lane, bool masked, uint32_t sees, State<C>& st) {
   typedef __attribute__((address_space(3))) const bf16x8* k_ptr;
   typedef __attribute__((address_space(3))) s16x4* tr_ptr;
-  const int h = lane >> 5;
+  f32x16 s = {};
 #pragma unroll
-  for (int sub = 0; sub < C::TK / 32; ++sub) {
-    f32x16 s = {};
+  for (int x = 0; x < C::D / 16; ++x) {
+    const bf16x8 kf = *(k_ptr)(kt + (at.k ^ (32 * x)));
+    s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[x], s, 0, 0, 0);
+  }
+  if (masked) {
+    const uint32_t bits = sees >> (4 * (lane >> 5));
 #pragma unroll
-    for (int x = 0; x < C::D / 16; ++x) {
-      const bf16x8 kf = *(k_ptr)(kt + (at.k ^ (32 * x)) + sub * 32 * C::kRowBytes);
-      s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[x], s, 0, 0, 0);
-    }
-    if (masked) {
-      const uint32_t bits = (uint32_t)(sees >> (32 * sub)) >> (4 * h);
+    for (int i = 0; i < 16; ++i) s[i] = (bits >> (8 * (i / 4) + i % 4)) & 1 ? s[i] : -INFINITY;
+  }
+  float top = s[0];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = (bits >> (8 * (i / 4) + i % 4)) & 1 ? s[i] : -INFINITY;
-    }
-    float top = s[0];
+  for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+  top = fmaxf(top, xor32(top, lane)) * c2;
+  // A row's maximum follows only when it lags by more than 2^8: weights are then at most
+  // 2^8 and nothing is lost, and most steps leave the sums alone.
+  if (__ballot(top > st.m + kLag)) {
+    const float m = fmaxf(st.m, top);
+    const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
+    st.l *= f;
 #pragma unroll
-    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-    top = fmaxf(top, xor32(top, lane)) * c2;
-    // A row's maximum follows only when it lags by more than 2^8: weights are then at most
-    // 2^8 and nothing is lost, and most steps leave the sums alone.
-    if (__ballot(top > st.m + kLag)) {
-      const float m = fmaxf(st.m, top);
-      const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
-      st.l *= f;
+    for (int dt = 0; dt < C::D / 32; ++dt)
 #pragma unroll
-      for (int dt = 0; dt < C::D / 32; ++dt)
+      for (int i = 0; i < 16; ++i) st.o[dt][i] *= f;
+    st.m = m;
+  }
+  const float m0 = st.m == -INFINITY ? 0.f : st.m;
+  float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) st.o[dt][i] *= f;
-      st.m = m;
-    }
-    const float m0 = st.m == -INFINITY ? 0.f : st.m;
-    float sum = 0.f;
+  for (int i = 0; i < 16; ++i) {
+    s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c2, -m0));
+    sum += s[i];
+  }
+  st.l += sum;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c2, -m0));
-      sum += s[i];
-    }
-    st.l += sum;
+  for (int kc = 0; kc < 2; ++kc) {
+    union {
+      bf16x2 two[4];
+      bf16x8 all;
+    } pf;
 #pragma unroll
-    for (int kc = 0; kc < 2; ++kc) {
+    for (int i = 0; i < 4; ++i)
+      pf.two[i] = __builtin_convertvector(f32x2{s[8 * kc + 2 * i], s[8 * kc + 2 * i + 1]}, bf16x2);
+#pragma unroll
+    for (int dt = 0; dt < C::D / 32; ++dt) {
       union {
-        bf16x2 two[4];
+        s16x4 half[2];
         bf16x8 all;
-      } pf;
+      } vf;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        pf.two[i] = __builtin_convertvector(f32x2{s[8 * kc + 2 * i], s[8 * kc + 2 * i + 1]}, bf16x2);
-#pragma unroll
-      for (int dt = 0; dt < C::D / 32; ++dt) {
-        union {
-          s16x4 half[2];
-          bf16x8 all;
-        } vf;
-#pragma unroll
-        for (int z = 0; z < 2; ++z)
-          vf.half[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (tr_ptr)(vt + at.v[dt] + (32 * sub + 16 * kc + 8 * z) * C::kRowBytes));
-        st.o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf.all, pf.all, st.o[dt], 0, 0, 0);
-      }
+      for (int z = 0; z < 2; ++z)
+        vf.half[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)(vt + at.v[dt] + (16 * kc + 8 * z) * C::kRowBytes));
+      st.o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf.all, pf.all, st.o[dt], 0, 0, 0);
     }
   }
+}
+
+// What the waves of a key group wrote to LDS is there for all of them.
+template <class C>
+__device__ __forceinline__ void group_sync() {
+  if constexpr (C::RW > 1)
+    big::bar();
+  else
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 }
 
 template <class C>
 __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kernel(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[C::kLds];
-  __shared__ int64_t scratch[C::kThreads + 2];
-  __shared__ int s_odd;
-  if (threadIdx.x == 0) s_odd = 0;
+  __shared__ int scratch[C::kThreads + 2];
+  __shared__ int s_odd[C::KW];
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
   const int kw = wave / C::RW, rw = wave % C::RW;
-  const int per_head = a.G * a.row_tiles;
-  const int head = blockIdx.x / per_head, rt = blockIdx.x % per_head % a.row_tiles,
-            g = blockIdx.x % per_head / a.row_tiles;
+  const int Hkv = a.c.kv_heads;
+  // Workgroups go round the eight XCDs in turn: the row tiles of a part are eight apart, so
+  // that they run side by side on one XCD and read the part's keys into its L2 once.
+  const int turn = blockIdx.x / (8 * a.row_tiles), rt = blockIdx.x / 8 % a.row_tiles;
+  const int unit = turn * 8 + blockIdx.x % 8;  // (head, part)
+  if (unit >= Hkv * a.G) return;
+  const int head = unit / a.G, g = unit % a.G;
   // part g of min(G, total): the tiles x .. x_end - 1, at least one
-  const Where w = locate<C::kThreads>(a, C::kTile, scratch, [&](int64_t total) {
-    return min(g * total / min((int64_t)a.G, total), total - 1);
+  const Where w = locate<C>(a, scratch, [&](int total) {
+    return min(mul_div(g, total, min(a.G, total)), total - 1);
   });
-  const int64_t parts = min((int64_t)a.G, w.total);
+  const int total = uniform(w.total), parts = min(a.G, total);
   if (g >= parts) return;
-  int64_t x = g * w.total / parts;
-  const int64_t x_end = (g + 1) * w.total / parts;
-  const int Hkv = a.c.kv_heads, rows = a.T * a.group;
+  int x = uniform(mul_div(g, total, parts));
+  const int x_end = uniform(mul_div(g + 1, total, parts));
+  const int rows = a.T * a.group;
   const int row = rt * C::kRows + 32 * rw + (lane & 31);
   const int qrow = min(row, rows - 1), t = qrow / a.group, gh = qrow % a.group;
   const int h = lane >> 5;
-  int seq = w.seq;
-  int64_t before = w.before;
+  int seq = uniform(w.seq), before = uniform(w.before);
   const int64_t slot0 = ((int64_t)head * a.row_tiles + rt) * 2 * a.G;
   const Frag<C> at(lane);
+  const uint32_t ring0 = lds_addr(lds) + kw * C::S * C::kStage;
+  const uint32_t pages0 = lds_addr(lds) + C::kRing + wave * (C::kAhead + 1) * C::kPages;
+  const char* ring = lds + kw * C::S * C::kStage;
+  const char* my_pages = lds + C::kRing + wave * (C::kAhead + 1) * C::kPages;
+  const int64_t page_bytes = ((int64_t)Hkv << a.c.page_shift) * C::kRowBytes;
 
   while (x < x_end) {
     const int len = a.c.len(seq);
-    const int tiles = seq_tiles(len, C::kTile);
-    const int first = (int)(x - before), last = (int)min((int64_t)tiles, x_end - before);
+    const int ctiles = cache_tiles<C>(len), tiles = ctiles + (a.T + C::kTile - 1) / C::kTile;
+    const int first = x - before, last = min(tiles, x_end - before);
+    const int n = last - first;  // steps
     const int32_t* table = a.c.block_table + (int64_t)seq * a.c.table_width;
+    // Pages of a step's keys or more: they lie in one, read by a scalar load a step ahead.
+    const bool wide = (1 << a.c.page_shift) >= C::kKeys;
+    auto wide_page = [&](int i) {
+      typedef const __attribute__((address_space(4))) int32_t* const_ptr;
+      const int key = min((first + i) * C::kTile + kw * C::kKeys, len - 1);
+      return *(const_ptr)(table + (max(key, 0) >> a.c.page_shift));
+    };
+    // Smaller ones: the pages of step i's keys, into its slot of this wave's ring.
+    auto look_up = [&](int i) {
+      const int key = min((first + i) * C::kTile + kw * C::kKeys + (lane & (C::kKeys - 1)), len - 1);
+      dma4(table + (max(key, 0) >> a.c.page_shift),
+           __builtin_amdgcn_readfirstlane(pages0 + i % (C::kAhead + 1) * C::kPages));
+    };
+    // This wave's share of step i's K and V rows.
+    auto load = [&](int i, int wide_id) {
+      const int tile = first + i;
+      const int rr = lane / C::kChunks, slot = lane % C::kChunks;
+      const uint32_t to = ring0 + i % C::S * C::kStage;
+      const int* pages = reinterpret_cast<const int*>(my_pages + i % (C::kAhead + 1) * C::kPages);
+      const bool tree = tile >= ctiles;
+      const char* k = tree ? reinterpret_cast<const char*>(a.k_new) : static_cast<const char*>(a.c.k_pages);
+      const char* v = tree ? reinterpret_cast<const char*>(a.v_new) : static_cast<const char*>(a.c.v_pages);
+      if (wide && !tree) {
+        // the step's first key; keys past the end read its page's rows of others, which are masked or cleared
+        const int key = tile * C::kTile + kw * C::kKeys;
+        const int page = min(max(wide_id, 0), a.c.n_pages - 1);
+        const int64_t off = (int64_t)page * page_bytes +
+                            (int64_t)((head << a.c.page_shift) + (key & ((1 << a.c.page_shift) - 1))) * C::kRowBytes;
+#pragma unroll
+        for (int u = 0; u < C::kLoads; ++u) {
+          int j = rw + C::RW * u;
+          if (C::kLoadsAll % C::RW != 0) j = min(j, C::kLoadsAll - 1);
+          const int row = j * C::kRowsPerLoad + rr;
+          dma16<C::kOnce>(k + off + row * C::kRowBytes + 16 * k_slot<C>(slot, row), __builtin_amdgcn_readfirstlane(to + j * 1024));
+          dma16<C::kOnce>(v + off + row * C::kRowBytes + 16 * v_slot<C>(slot, row),
+                __builtin_amdgcn_readfirstlane(to + C::kHalf + j * 1024));
+        }
+        return;
+      }
+#pragma unroll
+      for (int u = 0; u < C::kLoads; ++u) {
+        int j = rw + C::RW * u;
+        if (C::kLoadsAll % C::RW != 0) j = min(j, C::kLoadsAll - 1);  // the last rows again
+        const int row = j * C::kRowsPerLoad + rr;
+        int64_t off;
+        if (tree) {
+          const int node = min((tile - ctiles) * C::kTile + kw * C::kKeys + row, a.T - 1);
+          off = (((int64_t)seq * a.T + node) * Hkv + head) * C::kRowBytes;
+        } else {
+          const int key = min(tile * C::kTile + kw * C::kKeys + row, len - 1);
+          const int page = min(max(pages[row], 0), a.c.n_pages - 1);
+          off = (int64_t)page * page_bytes +
+                (int64_t)((head << a.c.page_shift) + (key & ((1 << a.c.page_shift) - 1))) * C::kRowBytes;
+        }
+        dma16<C::kOnce>(k + off + 16 * k_slot<C>(slot, row), __builtin_amdgcn_readfirstlane(to + j * 1024));
+        dma16<C::kOnce>(v + off + 16 * v_slot<C>(slot, row), __builtin_amdgcn_readfirstlane(to + C::kHalf + j * 1024));
+      }
+    };
+    if (!wide) {
+#pragma unroll 1
+      for (int i = 0; i < C::S - 1; ++i) look_up(i);
+    }
     const int64_t qoff = (((int64_t)seq * a.T + t) * Hkv * a.group + head * a.group + gh) * C::D;
     bf16x8 qf[C::D / 16];
 #pragma unroll
     for (int i = 0; i < C::D / 16; ++i) qf[i] = *reinterpret_cast<const bf16x8*>(a.q + qoff + 16 * i + 8 * h);
+    uint64_t sees = 0, used = 0;  // of this lane's row; all used nodes
+    if (last > ctiles) {
+      const uint64_t bits = tree_bits(a.parents + (int64_t)seq * a.T, a.T, lane);
+      sees = shfl64(bits, t);
+      used = __ballot(bits != 0);
+    }
     State<C> st;
 #pragma unroll
     for (int dt = 0; dt < C::D / 32; ++dt) st.o[dt] = f32x16{};
     st.m = -INFINITY;
     st.l = 0.f;
-    const uint64_t bits = tree_bits(a.parents + (int64_t)seq * a.T, a.T, lane);
-    const uint64_t sees = shfl64(bits, t);  // this lane's row
-    const uint64_t used = __ballot(bits != 0);
-
-    // the page of this lane's key of a tile; looked up one step before its loads
-    auto page_of = [&](int tile) {
-      const int key = min(tile * C::kTile + kw * C::TK + (lane & (C::TK - 1)), len - 1);
-      return key >= 0 ? table[key >> a.c.page_shift] : 0;
-    };
-    auto load = [&](int tile, int pages, char* stage) {
-      char* grp = stage + kw * 2 * C::kHalf;
-      if (tile < tiles - 1) {
-        load_tile<C>(grp, rw, lane, [&](int k, bool isv) {
-          const int key = min(tile * C::kTile + kw * C::TK + k, len - 1);
-          const int page = min(max(__shfl(pages, k), 0), a.c.n_pages - 1);
-          const int64_t at = (((int64_t)page * Hkv + head) << a.c.page_shift) + (key & ((1 << a.c.page_shift) - 1));
-          return static_cast<const char*>(isv ? a.c.v_pages : a.c.k_pages) + at * C::kRowBytes;
-        });
-      } else {
-        load_tile<C>(grp, rw, lane, [&](int k, bool isv) {
-          const int node = min(kw * C::TK + k, a.T - 1);
-          const int64_t at = ((int64_t)seq * a.T + node) * Hkv + head;
-          return reinterpret_cast<const char*>(isv ? a.v_new : a.k_new) + at * C::kRowBytes;
-        });
+    big::wait_vmcnt<0>();
+    asm volatile("" ::: "memory");
+    int next_page = wide ? wide_page(0) : 0;
+#pragma unroll 1
+    for (int i = 1 - C::S; i < n; ++i) {
+      if (i >= 0) {
+        // step i's rows are here, and the pages of step i + S - 1; everyone is done with the stage before
+        if (i + C::S - 1 <= n)
+          big::wait_vmcnt<C::kInFlight>();
+        else
+          big::wait_vmcnt<0>();
+        group_sync<C>();
       }
-    };
-    load(first, page_of(first), lds);
-    int pages = page_of(min(first + 1, tiles - 1));
-    for (int i = first; i < last; ++i) {
-      char* stage = lds + ((i - first) & 1) * C::kStage;
-      // the tile and the pages of the next one are here; everyone is done with the other stage
-      big::wait_vmcnt<0>();
-      big::bar();
-      if (i + 1 < last) load(i + 1, pages, lds + ((i + 1 - first) & 1) * C::kStage);
-      pages = page_of(min(i + 2, tiles - 1));
-      char* kt = stage + kw * 2 * C::kHalf;
+      if (i + C::S - 1 < n) {
+        if (!wide) look_up(i + C::kAhead);
+        load(i + C::S - 1, next_page);
+        if (wide) next_page = wide_page(i + C::S);
+      }
+      if (i < 0) continue;
+      char* kt = const_cast<char*>(ring) + i % C::S * C::kStage;
       char* vt = kt + C::kHalf;
-      const int left = i < tiles - 1 ? len - i * C::kTile - kw * C::TK : a.T - kw * C::TK;  // keys that there are
-      const bool tree = i == tiles - 1;
+      const int tile = first + i;
+      const bool tree = tile >= ctiles;
+      const int base = (tree ? tile - ctiles : tile) * C::kTile + kw * C::kKeys;  // first key (or node)
+      const int left = (tree ? a.T : len) - base;                                // that there are from there on
       bool masked = false;
       uint64_t see = ~0ull;
-      if (tree || len - i * C::kTile < C::kTile) {
-        // the tree's tile, or the cache's last one
+      if (tree || left < C::kKeys) {
         masked = true;
         uint64_t there = left >= 64 ? ~0ull : left > 0 ? (1ull << left) - 1 : 0;
         see = there;
         if (tree) {
-          const bool any = left > 0;
-          there = any ? used >> (kw * C::TK) : 0;
-          see = any ? sees >> (kw * C::TK) : 0;
+          there = left > 0 ? used >> base : 0;
+          see = left > 0 ? sees >> base : 0;
         }
         const bool odd = clear_rows<C>(vt, rw, lane, there, tree);
-        if (__ballot(odd) && lane == 0) s_odd = 1;
-        big::bar();
+        if (rw == 0 && lane == 0) s_odd[kw] = 0;
+        group_sync<C>();
+        if (__ballot(odd) && lane == 0) s_odd[kw] = 1;
+        group_sync<C>();
       }
-      if (left > 0) step<C>((lds_t)kt, (lds_t)vt, at, qf, a.c2, lane, masked, see, st);
-      if (tree && s_odd && left > 0) {
+#pragma unroll
+      for (int sub = 0; sub < C::SUB; ++sub)
+        if (left > 32 * sub)
+          step<C>((lds_t)kt + sub * 32 * C::kRowBytes, (lds_t)vt + sub * 32 * C::kRowBytes, at, qf, a.c2, lane, masked,
+                  (uint32_t)(see >> (32 * sub)), st);
+      if (tree && left > 0 && s_odd[kw]) {
         // what is not finite in a node's V (cleared above) reaches the rows that see the node, and no others
 #pragma unroll 1
-        for (int k = 0; k < min(C::TK, left); ++k) {
-          const uint16_t* v = a.v_new + (((int64_t)seq * a.T + kw * C::TK + k) * Hkv + head) * C::D;
+        for (int k = 0; k < min(C::kKeys, left); ++k) {
+          const uint16_t* v = a.v_new + (((int64_t)seq * a.T + base + k) * Hkv + head) * C::D;
           const bool on = (see >> k) & 1;
 #pragma unroll
           for (int dt = 0; dt < C::D / 32; ++dt) {
@@ -476,121 +589,160 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
       }
     }
     __syncthreads();
-    if (threadIdx.x == 0) s_odd = 0;
     x = before + last;
     before += tiles;
     ++seq;
   }
 }
 
-// Sequences cut over several workgroups: their pieces joined.  Workgroup (sequence, kv head).
+// Sequences cut over several workgroups: their pieces joined, 16 (or 4) query rows a
+// workgroup.  16 lanes hold a row's D values.  Few pieces: a row for each 16 lanes; many: a
+// row for a wave, each 16 lanes every fourth piece.  All pieces' loads are independent, so that a row
+// takes a few memory latencies however many pieces it has.
 template <class C>
 __global__ __launch_bounds__(256) void tree_attention_join_kernel(AttnArgs a) {
-  __shared__ int64_t scratch[256 + 2];
-  __shared__ int s_used[kMaxNodes];
-  const int Hkv = a.c.kv_heads;
-  const int seq = blockIdx.x / Hkv, head = blockIdx.x % Hkv;
-  // tiles before this sequence
-  const int per = (a.batch + 255) / 256;
-  int64_t mine = 0, upto = 0;
-  for (int b = threadIdx.x * per; b < min((int)(threadIdx.x + 1) * per, a.batch); ++b) {
-    const int n = seq_tiles(a.c.len(b), C::kTile);
-    mine += n;
-    if (b < seq) upto += n;
-  }
-  // two sums over the threads
-  auto sum = [&](int64_t v) {
-    scratch[threadIdx.x] = v;
-    __syncthreads();
-    for (int s = 128; s > 0; s >>= 1) {
-      if ((int)threadIdx.x < s) scratch[threadIdx.x] += scratch[threadIdx.x + s];
-      __syncthreads();
+  constexpr int kPer = C::D / 16;  // values of a lane
+  __shared__ int scratch[8];
+  const bool many = a.many;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int Hkv = a.c.kv_heads, rows = a.T * a.group;
+  const int each = many ? 4 : 16, chunks = (rows + each - 1) / each;
+  const int seq = blockIdx.x / (Hkv * chunks), head = blockIdx.x / chunks % Hkv;
+  const int row0 = blockIdx.x % chunks * each;
+  // all tiles, and those before this sequence
+  int total, before;
+  if (a.batch == 1) {
+    total = seq_tiles<C>(a, 0), before = 0;
+  } else if (a.batch <= 64) {
+    total = lane < a.batch ? seq_tiles<C>(a, lane) : 0;
+    before = lane < seq ? total : 0;
+#pragma unroll
+    for (int j = 32; j > 0; j >>= 1) {
+      total += (int)xor_lanes((uint32_t)total, j, lane);
+      before += (int)xor_lanes((uint32_t)before, j, lane);
     }
-    const int64_t r = scratch[0];
+  } else {
+    int mine = 0, upto = 0;
+    for (int b = threadIdx.x; b < a.batch; b += 256) {
+      const int n = seq_tiles<C>(a, b);
+      mine += n;
+      if (b < seq) upto += n;
+    }
+    for (int j = 32; j > 0; j >>= 1) {
+      mine += (int)xor_lanes((uint32_t)mine, j, lane);
+      upto += (int)xor_lanes((uint32_t)upto, j, lane);
+    }
+    if (lane == 0) scratch[wave] = mine, scratch[4 + wave] = upto;
     __syncthreads();
-    return r;
-  };
-  const int64_t total = sum(mine), before = sum(upto);
-  const int tiles = seq_tiles(a.c.len(seq), C::kTile);
-  const int64_t parts = min((int64_t)a.G, total);  // and the first and last of them with a tile of this sequence
-  const int g0 = (int)(((before + 1) * parts - 1) / total), g1 = (int)(((before + tiles) * parts - 1) / total);
+    total = scratch[0] + scratch[1] + scratch[2] + scratch[3];
+    before = scratch[4] + scratch[5] + scratch[6] + scratch[7];
+  }
+  const int tiles = seq_tiles<C>(a, seq), parts = min(a.G, total);
+  // the first and the last part with a tile of this sequence: tile y is in part
+  // floor(((y + 1) parts - 1) / total)
+  auto part_of = [&](int y) { return uniform((int)(((double)(y + 1) * (double)parts - 1.0) / (double)total)); };
+  const int g0 = part_of(before), g1 = part_of(before + tiles - 1);
   if (g0 == g1) return;  // one piece: written already
-  if (threadIdx.x < 64) s_used[threadIdx.x] = tree_bits(a.parents + (int64_t)seq * a.T, a.T, threadIdx.x) != 0;
-  __syncthreads();
-  const int rows = a.T * a.group;
-  for (int u = threadIdx.x; u < rows * (C::D / 4); u += 256) {
-    const int row = u / (C::D / 4), d = u % (C::D / 4) * 4;
-    const int rt = row / C::kRows, rr = row % C::kRows;
-    const int64_t slot0 = ((int64_t)head * a.row_tiles + rt) * 2 * a.G;
-    auto slot = [&](int g) { return (slot0 + 2 * g + (g == g0 ? 1 : 0)) * C::kRows + rr; };
+  const uint64_t bits = tree_bits(a.parents + (int64_t)seq * a.T, a.T, lane);
+  const int quarter = lane >> 4;
+  {
+    const int row = row0 + (many ? wave : 4 * wave + quarter);
+    const int qrow = min(row, rows - 1), t = qrow / a.group;
+    const bool used = shfl64(bits, t) != 0;
+    const int64_t slot0 = ((int64_t)head * a.row_tiles + qrow / C::kRows) * 2 * a.G;
+    auto slot = [&](int g) { return (slot0 + 2 * g + (g == g0 ? 1 : 0)) * C::kRows + qrow % C::kRows; };
     float m = -INFINITY;
-    for (int g = g0; g <= g1; ++g) m = fmaxf(m, a.part_ml[2 * slot(g)]);
-    float l = 0.f;
-    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    if (many) {
+      for (int g = g0 + lane; g <= g1; g += 64) m = fmaxf(m, a.part_ml[2 * slot(g)]);
+#pragma unroll
+      for (int j = 32; j > 0; j >>= 1) m = fmaxf(m, __uint_as_float(xor_lanes(__float_as_uint(m), j, lane)));
+    } else {
+#pragma unroll 4
+      for (int g = g0; g <= g1; ++g) m = fmaxf(m, a.part_ml[2 * slot(g)]);
+    }
     const float m0 = m == -INFINITY ? 0.f : m;
-    for (int g = g0; g <= g1; ++g) {
+    float l = 0.f, o[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int g = g0 + (many ? quarter : 0); g <= g1; g += many ? 4 : 1) {
       const f32x2 ml = *reinterpret_cast<const f32x2*>(a.part_ml + 2 * slot(g));
+      const float* p = a.part_o + slot(g) * C::D + (lane & 15) * kPer;
       const float f = __builtin_amdgcn_exp2f(ml.x - m0);
       l += ml.y * f;
-      const f32x4 p = *reinterpret_cast<const f32x4*>(a.part_o + slot(g) * C::D + d);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] += p[i] * f;
+      for (int e = 0; e < kPer; e += 4) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(p + e);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) o[e + z] += v[z] * f;
+      }
     }
-    const int t = row / a.group;
-    const bool some = s_used[t] && l != 0.f;
-    const float inv = some ? 1.0f / l : 0.f;
-    float v[4];
+    if (many) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = some ? o[i] * inv : 0.f;
-    const bf16x2 lo = __builtin_convertvector(f32x2{v[0], v[1]}, bf16x2);
-    const bf16x2 hi = __builtin_convertvector(f32x2{v[2], v[3]}, bf16x2);
+      for (int j = 16; j <= 32; j += 16) {
+        l += __uint_as_float(xor_lanes(__float_as_uint(l), j, lane));
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[e] += __uint_as_float(xor_lanes(__float_as_uint(o[e]), j, lane));
+      }
+    }
+    if (row >= rows || (many && quarter > 0)) return;
+    const bool some = used && l != 0.f;
+    const float inv = some ? 1.0f / l : 0.f;
     union {
-      bf16x2 b[2];
-      uint2 u;
+      bf16x2 b[kPer / 2];
+      uint2 u[kPer / 4];
     } pk;
-    pk.b[0] = lo;
-    pk.b[1] = hi;
-    *reinterpret_cast<uint2*>(a.out + (((int64_t)seq * a.T + t) * Hkv * a.group + head * a.group + row % a.group) * C::D +
-                              d) = pk.u;
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2)
+      pk.b[e / 2] = __builtin_convertvector(some ? f32x2{o[e] * inv, o[e + 1] * inv} : f32x2{0.f, 0.f}, bf16x2);
+    uint16_t* out = a.out + (((int64_t)seq * a.T + t) * Hkv * a.group + head * a.group + row % a.group) * C::D +
+                    (lane & 15) * kPer;
+#pragma unroll
+    for (int e = 0; e < kPer / 4; ++e) reinterpret_cast<uint2*>(out)[e] = pk.u[e];
   }
 }
 
 template <class C>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
-  tree_attention_kernel<C><<<dim3((uint32_t)(a.G * a.row_tiles * a.c.kv_heads)), dim3(C::kThreads), 0, stream>>>(a);
+  tree_attention_kernel<C><<<dim3((uint32_t)(cdiv((int64_t)a.G * a.c.kv_heads, 8) * 8 * a.row_tiles)), dim3(C::kThreads), 0, stream>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.G == 1) return e;
-  tree_attention_join_kernel<C><<<dim3((uint32_t)(a.batch * a.c.kv_heads)), dim3(256), 0, stream>>>(a);
+  tree_attention_join_kernel<C><<<
+      dim3((uint32_t)(a.batch * a.c.kv_heads * cdiv(a.T * a.group, a.many ? 4 : 16))), dim3(256), 0, stream>>>(a);
   return hipGetLastError();
 }
 
-// Few rows: waves take keys of their own; more rows: they share the keys.
-template <int D>
-hipError_t launch_d(int kind, const AttnArgs& a, hipStream_t stream) {
-  switch (kind) {
-    case 0: return launch<Cfg<D, 4, 1, 32>>(a, stream);
-    case 1: return launch<Cfg<D, 2, 2, 32>>(a, stream);
-    case 2: return launch<Cfg<D, 1, 3, 64>>(a, stream);
-    default: return launch<Cfg<D, 1, 4, 64>>(a, stream);
-  }
+// Query rows of a head, and the configurations that take them: up to 32 the waves have keys
+// of their own; more rows share them, 128 to a workgroup.  64 keys a step and two stages
+// against 32 keys and four (a barrier for every 16 KB): 213 us against 229 at 64 sequences x 17
+// nodes x 8192 keys, head 128; 155 against 171 at 2 x 64 nodes x 131001 keys, head 64.
+template <int D, class F>
+auto with_cfg(int64_t rows, F f) {
+  if (rows <= 32) return f(Cfg<D, 4, 1, D == 64 ? 3 : 2, 1>{});
+  if (rows <= 64) return f(Cfg<D, 1, 2, 2, 2>{});
+  if (rows <= 96) return f(Cfg<D, 1, 3, 2, 2>{});
+  return f(Cfg<D, 1, 4, 2, 2>{});
 }
 
 }  // namespace
 
 AttnPlan plan_tree_attention(const CacheView& c, int64_t batch, int64_t T, int64_t group, int64_t D) {
-  AttnPlan p{};
   const int64_t rows = T * group;
-  p.kind = rows <= 32 ? 0 : rows <= 64 ? 1 : rows <= 96 ? 2 : 3;
-  p.tile_rows = p.kind == 0 ? 32 : p.kind == 1 ? 64 : p.kind == 2 ? 96 : 128;
-  p.row_tiles = cdiv(rows, p.tile_rows);
-  const int64_t tile = p.kind == 0 ? 128 : 64;
-  const int64_t most = batch * (cdiv((int64_t)c.table_width << c.page_shift, tile) + 1);  // tiles, all lengths full
-  p.G = kAttnBlocks / (p.row_tiles * c.kv_heads);
-  p.G = p.G < 1 ? 1 : p.G > most ? most : p.G;
-  const int64_t slots = (int64_t)c.kv_heads * p.row_tiles * 2 * p.G * p.tile_rows;
-  p.part_bytes = p.G > 1 ? align_up((size_t)(slots * D) * 4, 256) : 0;
-  p.ws_bytes = p.G > 1 ? p.part_bytes + align_up((size_t)slots * 8, 256) : 0;
-  return p;
+  auto plan = [&](auto cfg) {
+    typedef decltype(cfg) C;
+    AttnPlan p{};
+    p.row_tiles = cdiv(rows, C::kRows);
+    // tiles when all lengths are full: no more parts than that
+    const int64_t most =
+        batch * (cdiv((int64_t)c.table_width << c.page_shift, C::kTile) + cdiv(T, (int64_t)C::kTile));
+    p.G = 256 * C::kGroups / (p.row_tiles * c.kv_heads);
+    p.G = p.G < 1 ? 1 : p.G > most ? most : p.G;
+    const int64_t slots = (int64_t)c.kv_heads * p.row_tiles * 2 * p.G * C::kRows;
+    p.part_bytes = p.G > 1 ? align_up((size_t)(slots * D) * 4, 256) : 0;
+    p.ws_bytes = p.G > 1 ? p.part_bytes + align_up((size_t)slots * 8, 256) : 0;
+    return p;
+  };
+  return D == 64 ? with_cfg<64>(rows, plan) : with_cfg<128>(rows, plan);
 }
 
 hipError_t launch_tree_attention(const AttnPlan& p, const CacheView& c, const void* q, const void* k_new,
@@ -610,8 +762,10 @@ hipError_t launch_tree_attention(const AttnPlan& p, const CacheView& c, const vo
   a.group = (int)group;
   a.G = (int)p.G;
   a.row_tiles = (int)p.row_tiles;
+  a.many = p.G >= 8 * batch;
   a.c2 = (float)(scale * 1.4426950408889634);
-  return D == 64 ? launch_d<64>(p.kind, a, stream) : launch_d<128>(p.kind, a, stream);
+  auto run = [&](auto cfg) { return launch<decltype(cfg)>(a, stream); };
+  return D == 64 ? with_cfg<64>(T * group, run) : with_cfg<128>(T * group, run);
 }
 
 }  // namespace dfs

@@ -602,7 +602,7 @@ int dfs_norm_q8(const void* x, const void* residual, const void* weight, dfs_dty
 
 static int check_linear_q8_shape(int64_t rows, int64_t N, int64_t K) {
   if (rows < 1 || rows > DFS_MAX_ROWS || N < 1 || N > kMaxV || K < 16 || K > kMaxD) return DFS_E_SHAPE;
-  if (cdiv(rows, 64) * cdiv(N, 64) > ((int64_t)1 << 23)) return DFS_E_SHAPE;
+  if (cdiv(rows, 64) * cdiv(N, 64) > ((int64_t)1 << 23) || N > ((int64_t)1 << 39) / K) return DFS_E_SHAPE;
   if (K % 16 != 0) return DFS_E_UNSUPPORTED;
   return DFS_OK;
 }
@@ -640,7 +640,8 @@ static int check_cache_shape(const dfs_cache_shape_t* s) {
   if (s->batch < 1 || s->batch > 65536 || s->T < 1 || s->T > DFS_MAX_NODES || s->kv_heads < 1 ||
       s->kv_heads > 1024 || s->batch * s->kv_heads > ((int64_t)1 << 22) || s->head_dim < 8 || s->head_dim > 1024 ||
       s->page_size < 1 || s->page_size > 65536 || s->n_pages < 1 || s->n_pages > kMaxV || s->table_width < 1 ||
-      s->table_width > ((int64_t)1 << 30) / s->page_size)
+      s->table_width > ((int64_t)1 << 30) / s->page_size ||
+      s->batch * (s->table_width * s->page_size + 128) > ((int64_t)1 << 36))
     return DFS_E_SHAPE;
   if ((s->page_size & (s->page_size - 1)) != 0 || s->head_dim % 8 != 0) return DFS_E_UNSUPPORTED;
   return DFS_OK;
@@ -649,7 +650,7 @@ static int check_cache_shape(const dfs_cache_shape_t* s) {
 static int check_attention_shape(const dfs_cache_shape_t* s) {
   const int st = check_cache_shape(s);
   if (st != DFS_OK) return st;
-  if (s->q_heads < 1 || s->q_heads > 1024) return DFS_E_SHAPE;
+  if (s->q_heads < 1 || s->q_heads > 1024 || s->batch * s->T * s->q_heads > ((int64_t)1 << 25)) return DFS_E_SHAPE;
   if (s->q_heads % s->kv_heads != 0 || (s->head_dim != 64 && s->head_dim != 128) || s->dtype != DFS_BF16)
     return DFS_E_UNSUPPORTED;
   return DFS_OK;

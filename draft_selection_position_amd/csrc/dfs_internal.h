@@ -222,11 +222,7 @@ hipError_t launch_cache_commit(const CacheView& c, const void* k_new, const void
                                const int32_t* counts, int64_t batch, int64_t T, int64_t P, int32_t* out_lens,
                                hipStream_t stream);
 
-// Workgroups of an attention launch: two for each of MI355X's 256 CUs.
-constexpr int64_t kAttnBlocks = 512;
 struct AttnPlan {
-  int kind;                // waves by key groups x row groups
-  int64_t tile_rows;       // query rows of a workgroup
   int64_t row_tiles;       // workgroups for a head's rows
   int64_t G;               // parts that the keys of a head are cut into
   size_t part_bytes;       // of the parts' fp32 sums; their maxima and sums follow

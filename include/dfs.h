@@ -353,13 +353,15 @@ int dfs_norm_q8(const void* x, const void* residual, const void* weight, dfs_dty
 
 /* ---------------------------------------------------------------- 8-bit product
  * out[r, n] = sum_g a_scale[g, r] w_scale[n / 128, g] sum_{k in group g} a[r, k] w[n, k]
- * over groups g of 128 k (the last may be shorter); products and sums in fp32, out rounded
- * once.  With w an LM head these are the logits that dfs_topk, dfs_select and dfs_verify read.
+ * over groups g of 128 k (the last may be shorter), out rounded once.  Sums in fp32; for
+ * out_dt DFS_BF16, but for few rows, a group's products go through the 8-bit matrix instruction,
+ * which loses what is 2^13 below the largest of eight neighbouring products (about 2e-5 of
+ * the result's 2-norm: a hundredth of the output's own rounding).  With w an LM head these are the logits that dfs_topk, dfs_select and dfs_verify read.
  *   a [rows, K], w [N, K] e4m3 (OCP); a_scale [ceil(K / 128), rows] (dfs_norm_q8's order) and
  *   w_scale [ceil(N / 128), ceil(K / 128)] fp32; out [rows, N] of dtype out_dt, not overlapping an
  *   input.
  * K a multiple of 16 in [16, DFS_MAX_D], 1 <= N < 2^31, 1 <= rows <= DFS_MAX_ROWS and
- * ceil(rows / 64) * ceil(N / 64) <= 2^23.  Alignment: a, w, out 16 bytes; scales 4; ws 256.
+ * ceil(rows / 64) * ceil(N / 64) <= 2^23, N * K <= 2^39.  Alignment: a, w, out 16 bytes; scales 4; ws 256.
  * ws: dfs_linear_q8_workspace_bytes(rows, N, K) bytes of scratch (may be 0, then ws may be
  * NULL).                                                                           */
 size_t dfs_linear_q8_workspace_bytes(int64_t rows, int64_t N, int64_t K);
@@ -375,12 +377,13 @@ int dfs_linear_q8(const uint8_t* a, const float* a_scale, const uint8_t* w, cons
 typedef struct {
   int64_t batch;       /* sequences, 1..65536, and batch * kv_heads <= 2^22 */
   int64_t T;           /* nodes per sequence, 1..DFS_MAX_NODES */
-  int64_t q_heads;     /* query heads, a multiple of kv_heads, <= 1024 */
+  int64_t q_heads;     /* query heads, a multiple of kv_heads, <= 1024, and batch * T * q_heads <= 2^25 */
   int64_t kv_heads;    /* >= 1; query head h reads kv head h / (q_heads / kv_heads) */
   int64_t head_dim;    /* 64 or 128 (dfs_cache_commit: a multiple of 8 in [8, 1024]) */
   int64_t page_size;   /* a power of two, 1..65536 */
   int64_t n_pages;     /* pages of the pool, 1..2^31-1 */
-  int64_t table_width; /* entries per sequence; table_width * page_size <= 2^30 */
+  int64_t table_width; /* entries per sequence; table_width * page_size <= 2^30, and
+                          batch * (table_width * page_size + 128) <= 2^36 */
   dfs_dtype_t dtype;   /* of q, keys, values and the output */
 } dfs_cache_shape_t;
 
