@@ -16,6 +16,7 @@ then walk the scores once from the last verified token.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -521,31 +522,52 @@ def lmhead_logits(hidden: torch.Tensor, W_lm: torch.Tensor, out: torch.Tensor | 
 
 
 # ---------------------------------------------------------------- verification pass
+#
+# These calls are short where few rows are decoded (a few microseconds on the GPU), so what is
+# checked on every call is one attribute each; the words for a refusal are found afterwards.
+
+_CODES = {torch.float32: F32, torch.bfloat16: BF16}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _same_device(device: torch.device, **tensors) -> None:
+def _fits(t, dtype, index: int) -> bool:
+    """Whether t is a contiguous tensor of dtype on HIP device `index`."""
+    return (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.get_device() == index
+            and t.is_contiguous())
+
+
+def _refuse(first: str, tensors: dict, dtypes: dict) -> None:
+    """Raises for the first of the named tensors that does not fit: a HIP device, contiguous, its dtype, and
+    the first one's device.  None of them is optional."""
+    device = None
     for what, t in tensors.items():
-        if t is not None and t.device != device:
+        _dev(t, what, dtypes.get(what))
+        if what == first:
+            device = t.device
+    for what, t in tensors.items():
+        if t.device != device:
             raise ValueError(f"{what} must be on {device}, got {t.device}")
 
 
-def _call(device: torch.device, where: str, fn, *args) -> None:
-    """fn(*args, stream) on the tensors' own device and its current stream."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(device)), where)
+def _call(index: int, where: str, fn, *args) -> None:
+    """fn(*args, stream) on HIP device `index` and its current stream."""
+    if index == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream(device)), where)
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
+    if rc != 0:
+        raise DfsError(rc, where)
 
 
-def _scratch(workspace, device: torch.device, nbytes: int):
+def _scratch(workspace, like: torch.Tensor, nbytes: int):
     """The workspace of a call: the caller's, or a new block of the current stream's (a graph's own under capture)."""
     if nbytes == 0:
         return None
     if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
     _dev(workspace, "workspace")
-    return _ws_arg(workspace, device, nbytes)
+    return _ws_arg(workspace, like.device, nbytes)
 
 
 def norm_q8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
@@ -555,35 +577,41 @@ def norm_q8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None
     x, residual [..., d] and weight [d], all bf16 or all fp32.  Returns (q e4m3 [..., d], scale fp32
     [ceil(d / 128), rows]), then with a residual the sum in x's dtype (written into ``total_out`` when
     given, which may be ``x`` or ``residual`` itself), then with ``normed=True`` the norm in x's dtype."""
-    _dev(x, "x")
-    dt = _dtype_code(x, "x")
-    _dev(weight, "weight", x.dtype)
-    if x.dim() < 1 or weight.shape != x.shape[-1:]:
+    if not isinstance(x, torch.Tensor) or x.dtype not in _CODES:
+        _dev(x, "x")
+        _dtype_code(x, "x")
+    dtype, index = x.dtype, x.get_device()
+    if not (_fits(x, dtype, index) and _fits(weight, dtype, index)
+            and (residual is None or _fits(residual, dtype, index))
+            and (total_out is None or _fits(total_out, dtype, index))):
+        given = {"x": x, "weight": weight, "residual": residual, "total_out": total_out}
+        given = {k: t for k, t in given.items() if k in ("x", "weight") or t is not None}
+        _refuse("x", given, dict.fromkeys(given, dtype))
+    shape = x.shape
+    if not shape or weight.shape != shape[-1:]:
         raise ValueError("x must be [..., d] and weight [d]")
-    _same_device(x.device, weight=weight, residual=residual, total_out=total_out)
     if residual is not None:
-        _dev(residual, "residual", x.dtype)
-        if residual.shape != x.shape:
+        if residual.shape != shape:
             raise ValueError("residual must have the shape of x")
-    if total_out is not None:
-        if residual is None:
-            raise ValueError("total_out needs a residual")
-        _dev(total_out, "total_out", x.dtype)
-        if total_out.shape != x.shape:
+        if total_out is None:
+            total_out = torch.empty_like(x)
+        elif total_out.shape != shape:
             raise ValueError("total_out must have the shape of x")
-    d = x.shape[-1]
+    elif total_out is not None:
+        raise ValueError("total_out needs a residual")
+    d = shape[-1]
     rows = x.numel() // d if d else 0
-    q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-    scale = torch.empty((-(-d // 128), rows), dtype=torch.float32, device=x.device)
-    total = None
-    if residual is not None:
-        total = torch.empty_like(x) if total_out is None else total_out
+    q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    scale = x.new_empty((-(-d // 128), rows), dtype=torch.float32)
     y = torch.empty_like(x) if normed else None
-    _call(x.device, "dfs_norm_q8", lib().dfs_norm_q8, x.data_ptr(), _ptr(residual), weight.data_ptr(), dt, rows, d,
-          float(eps), q.data_ptr(), scale.data_ptr(), _ptr(total), _ptr(y))
-    return (q, scale) + ((total,) if residual is not None else ()) + ((y,) if normed else ())
+    _call(index, "dfs_norm_q8", lib().dfs_norm_q8, x.data_ptr(), _ptr(residual), weight.data_ptr(), _CODES[dtype], rows,
+          d, eps, q.data_ptr(), scale.data_ptr(), _ptr(total_out), _ptr(y))
+    if residual is None:
+        return (q, scale, y) if normed else (q, scale)
+    return (q, scale, total_out, y) if normed else (q, scale, total_out)
 
 
+@functools.lru_cache(maxsize=1024)
 def linear_q8_workspace_bytes(rows: int, N: int, K: int) -> int:
     return int(lib().dfs_linear_q8_workspace_bytes(rows, N, K))
 
@@ -595,11 +623,16 @@ def linear_q8(q: torch.Tensor, scale: torch.Tensor, W: torch.Tensor, W_scale: to
 
     q [..., K] e4m3 with scale [ceil(K / 128), rows] fp32 (``norm_q8``'s); W [N, K] e4m3 with W_scale
     [ceil(N / 128), ceil(K / 128)] fp32.  ``out_dtype`` bf16 or fp32."""
-    _dev(q, "q", torch.float8_e4m3fn)
-    _dev(scale, "scale", torch.float32)
-    _dev(W, "W", torch.float8_e4m3fn)
-    _dev(W_scale, "W_scale", torch.float32)
-    if q.dim() < 1 or W.dim() != 2 or W.shape[1] != q.shape[-1]:
+    e4m3, f32 = torch.float8_e4m3fn, torch.float32
+    index = q.get_device() if isinstance(q, torch.Tensor) else -1
+    if not (_fits(q, e4m3, index) and _fits(scale, f32, index) and _fits(W, e4m3, index)
+            and _fits(W_scale, f32, index) and (out is None or _fits(out, out_dtype, index))):
+        given = {"q": q, "scale": scale, "W": W, "W_scale": W_scale} | ({} if out is None else {"out": out})
+        _refuse("q", given, {"q": e4m3, "scale": f32, "W": e4m3, "W_scale": f32, "out": out_dtype})
+    if out_dtype not in _CODES:
+        raise ValueError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
+    shape = q.shape
+    if not shape or W.dim() != 2 or W.shape[1] != shape[-1]:
         raise ValueError("q must be [..., K] and W [N, K]")
     N, K = W.shape
     rows = q.numel() // K if K else 0
@@ -607,43 +640,48 @@ def linear_q8(q: torch.Tensor, scale: torch.Tensor, W: torch.Tensor, W_scale: to
     if scale.shape != (G, rows) or W_scale.shape != (-(-N // 128), G):
         raise ValueError(f"scale must be [{G}, {rows}] and W_scale [{-(-N // 128)}, {G}]")
     if out is None:
-        out = torch.empty(tuple(q.shape[:-1]) + (N,), dtype=out_dtype, device=q.device)
-    else:
-        _dev(out, "out", out_dtype)
-        if out.shape != tuple(q.shape[:-1]) + (N,):
-            raise ValueError("out must be [..., N]")
-    _same_device(q.device, scale=scale, W=W, W_scale=W_scale, out=out)
-    nb = int(lib().dfs_linear_q8_workspace_bytes(rows, N, K))
-    ws = _scratch(workspace, q.device, nb)
-    _call(q.device, "dfs_linear_q8", lib().dfs_linear_q8, q.data_ptr(), scale.data_ptr(), W.data_ptr(),
-          W_scale.data_ptr(), rows, N, K, _dtype_code(out, "out"), out.data_ptr(), _ptr(ws), nb)
+        out = scale.new_empty(shape[:-1] + (N,), dtype=out_dtype)
+    elif out.shape != shape[:-1] + (N,):
+        raise ValueError("out must be [..., N]")
+    nb = linear_q8_workspace_bytes(rows, N, K)
+    ws = _scratch(workspace, q, nb)
+    _call(index, "dfs_linear_q8", lib().dfs_linear_q8, q.data_ptr(), scale.data_ptr(), W.data_ptr(), W_scale.data_ptr(),
+          rows, N, K, _CODES[out_dtype], out.data_ptr(), _ptr(ws), nb)
     return out
 
 
-def _cache_args(k_new, v_new, k_pages, v_pages, block_table, lens, q_heads=None) -> _CacheShape:
-    _dev(k_new, "k_new")
-    dt = _dtype_code(k_new, "k_new")
-    _dev(v_new, "v_new", k_new.dtype)
-    _dev(k_pages, "k_pages", k_new.dtype)
-    _dev(v_pages, "v_pages", k_new.dtype)
-    _dev(block_table, "block_table", torch.int32)
-    _dev(lens, "lens", torch.int32)
-    if k_new.dim() != 4 or v_new.shape != k_new.shape:
+@functools.lru_cache(maxsize=1024)
+def _cache_shape(batch, T, q_heads, kv_heads, head_dim, page_size, n_pages, table_width, dt):
+    """A call's sizes as the library takes them (a reference that is read during calls only), and the bytes
+    of scratch that attention over them needs."""
+    s = _CacheShape(batch, T, q_heads, kv_heads, head_dim, page_size, n_pages, table_width, dt)
+    return ctypes.byref(s), int(lib().dfs_tree_attention_workspace_bytes(ctypes.byref(s)))
+
+
+def _cache_sizes(k_new, v_new, k_pages, v_pages, block_table, lens, index):
+    """(batch, T, kv_heads, head_dim, page_size, n_pages, table_width, dtype code) of a call on a paged cache."""
+    dtype, i32 = k_new.dtype, torch.int32
+    if not (dtype in _CODES and _fits(k_new, dtype, index) and _fits(v_new, dtype, index)
+            and _fits(k_pages, dtype, index) and _fits(v_pages, dtype, index) and _fits(block_table, i32, index)
+            and _fits(lens, i32, index)):
+        _dev(k_new, "k_new")
+        _dtype_code(k_new, "k_new")
+        given = {"k_new": k_new, "v_new": v_new, "k_pages": k_pages, "v_pages": v_pages, "block_table": block_table,
+                 "lens": lens}
+        _refuse("k_new", given, dict.fromkeys(given, dtype) | {"block_table": i32, "lens": i32})
+    new, pages, table = k_new.shape, k_pages.shape, block_table.shape
+    if len(new) != 4 or v_new.shape != new:
         raise ValueError("k_new and v_new must both be [batch, T, kv_heads, head_dim]")
-    batch, T, Hkv, D = k_new.shape
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or k_pages.shape[1] != Hkv or k_pages.shape[3] != D:
-        raise ValueError(f"k_pages and v_pages must both be [n_pages, {Hkv}, page_size, {D}]")
-    if block_table.dim() != 2 or block_table.shape[0] != batch or lens.shape != (batch,):
-        raise ValueError(f"block_table must be [{batch}, width] and lens [{batch}]")
-    _same_device(k_new.device, v_new=v_new, k_pages=k_pages, v_pages=v_pages, block_table=block_table, lens=lens)
-    return _CacheShape(batch, T, Hkv if q_heads is None else q_heads, Hkv, D, k_pages.shape[2], k_pages.shape[0],
-                       block_table.shape[1], dt)
+    if len(pages) != 4 or v_pages.shape != pages or pages[1] != new[2] or pages[3] != new[3]:
+        raise ValueError(f"k_pages and v_pages must both be [n_pages, {new[2]}, page_size, {new[3]}]")
+    if len(table) != 2 or table[0] != new[0] or lens.shape != new[:1]:
+        raise ValueError(f"block_table must be [{new[0]}, width] and lens [{new[0]}]")
+    return new[0], new[1], new[2], new[3], pages[2], pages[0], table[1], _CODES[dtype]
 
 
 def tree_attention_workspace_bytes(batch: int, T: int, q_heads: int, kv_heads: int, head_dim: int, page_size: int,
                                    n_pages: int, table_width: int) -> int:
-    s = _CacheShape(batch, T, q_heads, kv_heads, head_dim, page_size, n_pages, table_width, BF16)
-    return int(lib().dfs_tree_attention_workspace_bytes(ctypes.byref(s)))
+    return _cache_shape(batch, T, q_heads, kv_heads, head_dim, page_size, n_pages, table_width, BF16)[1]
 
 
 def tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, parents: torch.Tensor,
@@ -656,27 +694,27 @@ def tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, pa
     parents [batch, T] int32 (-1: child of the cache's last token; -2: unused node); k_pages, v_pages
     [n_pages, kv_heads, page_size, D]; block_table [batch, width] int32; lens [batch] int32.  ``scale``
     defaults to D ** -0.5.  Returns [batch, T, q_heads, D]."""
-    _dev(q, "q", torch.bfloat16)
-    _dev(parents, "parents", torch.int32)
-    if q.dim() != 4:
-        raise ValueError("q must be [batch, T, q_heads, head_dim]")
-    s = _cache_args(k_new, v_new, k_pages, v_pages, block_table, lens, q.shape[2])
-    if q.dtype != k_new.dtype or q.shape[:2] != k_new.shape[:2] or q.shape[3] != s.head_dim:
-        raise ValueError("q must have k_new's dtype, batch, T and head_dim")
-    if parents.shape != q.shape[:2]:
+    bf16 = torch.bfloat16
+    index = q.get_device() if isinstance(q, torch.Tensor) else -1
+    if not (_fits(q, bf16, index) and _fits(parents, torch.int32, index) and isinstance(k_new, torch.Tensor)
+            and (out is None or _fits(out, bf16, index))):
+        given = {"q": q, "k_new": k_new, "parents": parents} | ({} if out is None else {"out": out})
+        _refuse("q", given, {"q": bf16, "k_new": bf16, "parents": torch.int32, "out": bf16})
+    batch, T, Hkv, D, page, n_pages, width, dt = _cache_sizes(k_new, v_new, k_pages, v_pages, block_table, lens, index)
+    shape = q.shape
+    if len(shape) != 4 or dt != BF16 or shape[0] != batch or shape[1] != T or shape[3] != D:
+        raise ValueError("q must be [batch, T, q_heads, head_dim], with k_new's dtype, batch, T and head_dim")
+    if parents.shape != shape[:2]:
         raise ValueError("parents must be [batch, T]")
     if out is None:
         out = torch.empty_like(q)
-    else:
-        _dev(out, "out", q.dtype)
-        if out.shape != q.shape:
-            raise ValueError("out must have the shape of q")
-    _same_device(q.device, k_new=k_new, parents=parents, out=out)
-    nb = int(lib().dfs_tree_attention_workspace_bytes(ctypes.byref(s)))
-    ws = _scratch(workspace, q.device, nb)
-    _call(q.device, "dfs_tree_attention", lib().dfs_tree_attention, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
-          parents.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
-          ctypes.byref(s), float(s.head_dim ** -0.5 if scale is None else scale), out.data_ptr(), _ptr(ws), nb)
+    elif out.shape != shape:
+        raise ValueError("out must have the shape of q")
+    s, nb = _cache_shape(batch, T, shape[2], Hkv, D, page, n_pages, width, dt)
+    ws = _scratch(workspace, q, nb)
+    _call(index, "dfs_tree_attention", lib().dfs_tree_attention, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+          parents.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), lens.data_ptr(), s,
+          D ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(ws), nb)
     return out
 
 
@@ -687,26 +725,29 @@ def cache_commit(k_new: torch.Tensor, v_new: torch.Tensor, nodes: torch.Tensor |
 
     k_new, v_new [batch, T, kv_heads, D]; nodes [batch, path_len] int32 (None: node i of a path is i);
     counts [batch] int32: nodes of the path to take.  Returns the new lengths (``lens`` stays as it is)."""
-    s = _cache_args(k_new, v_new, k_pages, v_pages, block_table, lens)
-    _dev(counts, "counts", torch.int32)
-    if counts.shape != (s.batch,):
+    i32 = torch.int32
+    index = counts.get_device() if isinstance(counts, torch.Tensor) else -1
+    if not (_fits(counts, i32, index) and isinstance(k_new, torch.Tensor) and (nodes is None or _fits(nodes, i32, index))
+            and (out_lens is None or _fits(out_lens, i32, index))):
+        given = {"counts": counts, "k_new": k_new, "nodes": nodes, "out_lens": out_lens}
+        given = {k: t for k, t in given.items() if k in ("counts", "k_new") or t is not None}
+        _refuse("counts", given, {"counts": i32, "nodes": i32, "out_lens": i32})
+    batch, T, Hkv, D, page, n_pages, width, dt = _cache_sizes(k_new, v_new, k_pages, v_pages, block_table, lens, index)
+    if counts.shape != lens.shape:
         raise ValueError("counts must be [batch]")
-    path = s.T
+    path = T
     if nodes is not None:
-        _dev(nodes, "nodes", torch.int32)
-        if nodes.dim() != 2 or nodes.shape[0] != s.batch:
+        if nodes.dim() != 2 or nodes.shape[0] != batch:
             raise ValueError("nodes must be [batch, path_len]")
         path = nodes.shape[1]
     if out_lens is None:
         out_lens = torch.empty_like(lens)
-    else:
-        _dev(out_lens, "out_lens", torch.int32)
-        if out_lens.shape != lens.shape:
-            raise ValueError("out_lens must be [batch]")
-    _same_device(k_new.device, nodes=nodes, counts=counts, out_lens=out_lens)
-    _call(k_new.device, "dfs_cache_commit", lib().dfs_cache_commit, k_new.data_ptr(), v_new.data_ptr(), _ptr(nodes),
-          counts.data_ptr(), path, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
-          ctypes.byref(s), out_lens.data_ptr())
+    elif out_lens.shape != lens.shape:
+        raise ValueError("out_lens must be [batch]")
+    s, _ = _cache_shape(batch, T, Hkv, Hkv, D, page, n_pages, width, dt)
+    _call(index, "dfs_cache_commit", lib().dfs_cache_commit, k_new.data_ptr(), v_new.data_ptr(), _ptr(nodes),
+          counts.data_ptr(), path, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), lens.data_ptr(), s,
+          out_lens.data_ptr())
     return out_lens
 
 

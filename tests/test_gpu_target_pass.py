@@ -8,7 +8,11 @@ eps / 2 of its type):
            the rounding of some value within that of the exact quotient.
   product  a block's 128 products are exact in fp32 and each addition in the matrix core is taken to keep
            2^-23 of the running sum's magnitude; then a multiply-add per block, 8 partial sums where K is
-           split, and the scales' product:  |err| <= (256 + 2 G + 12) u sum |a w| scales.
+           split, and the scales' product:  |err| <= (256 + 2 G + 12) u sum |a w| scales.  A bf16 output may
+           come from the 8-bit matrix instruction, which adds products by eight, aligned to the largest of
+           them, and drops what lies 2^13 or more below it: at most 7 x 2^-13 of each eight's largest, so
+           2^-10 sum |a w| scales.  Its errors are as often above as below; the sum of squares is held to
+           what rounding to bf16 gives, 2^-8 of each value, halved.
   attention  weights rounded to bf16: 2^-8 of sum w |v|.  A score's error (D + 4) u sum |q k| scale and the
            exponential's argument (rounded once, below 2^7 in size: 2^7 u) change a weight by that much
            relative, numerator and denominator: twice.  Sums over n keys: 2 n u.  The output: 2^-8.
@@ -141,8 +145,11 @@ def check_linear(dfs, g, rows, N, K, dtype):
     w, sw = quantised(g, N, K, 128, 0.05)
     out = dfs.linear_q8(a, sa, w, sw, out_dtype=dtype)
     want, mag = tp.linear_q8(f64(a), f64(sa), f64(w), f64(sw))
-    tol = (256 + 2 * -(-K // 128) + 12) * U * mag + torch.finfo(dtype).eps / 2 * np.abs(want) + 1e-38
+    lost = 2.0 ** -10 if dtype == torch.bfloat16 else (256 + 2 * -(-K // 128) + 12) * U
+    tol = lost * mag + torch.finfo(dtype).eps / 2 * np.abs(want) + 1e-38
     err = np.abs(f64(out) - want)
+    if dtype == torch.bfloat16:
+        assert np.linalg.norm(err) <= 2.0 ** -9 * np.linalg.norm(want) + 1e-38
     assert out.shape == (rows, N) and out.dtype == dtype
     far = (err / tol).max()
     assert far <= 1, far
