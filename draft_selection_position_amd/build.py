@@ -28,10 +28,12 @@ COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-Wno-unused-result",
           f"-I{os.path.join(ROOT, 'include')}"]
 
 
-# Of single sources.  attention.hip: matrix products with their sums in ordinary registers; where
-# only one wave fits a SIMD the compiler would keep them in accumulation registers and copy
-# them back and forth (750 copies in the kernel for few rows).
-SOURCE_FLAGS = {"attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+# Of single sources: matrix products with their sums in ordinary registers, where vector
+# instructions use them next.  The compiler would keep some in accumulation registers and copy
+# them back and forth (attention for few rows: 750 copies, 17.8 us against 15.1 for one token;
+# the 8-bit product in 128 x 128 tiles: 88 us against 84).
+_SUMS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+SOURCE_FLAGS = {"attention.hip": _SUMS, "linear.hip": _SUMS}
 
 
 def hipcc() -> str:

@@ -36,6 +36,7 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
+constexpr float kUnused = -1.0f;  // for a sum of weights
 constexpr float kLag = 8.0f;  // a maximum may lag this far (in powers of two) before sums are rescaled
 
 struct AttnArgs {
@@ -46,9 +47,10 @@ struct AttnArgs {
   const int32_t* parents;
   uint16_t* out;
   float* part_o;   // [Hkv, row tiles, 2 G, rows of a tile, D]
-  float* part_ml;  // [Hkv, row tiles, 2 G, rows of a tile, 2]
+  float* part_ml;  // [Hkv, row tiles, 2 G, rows of a tile, 2]: maximum and sum; of an unused node's row the last piece has kUnused
+  int2* pieces;    // [batch]: the first and the last part with a tile of the sequence
   int batch, T, group, G, row_tiles;
-  bool many;  // parts a sequence is cut into: eight or more, as a rule
+  int spread;  // 16-lane groups that join a row's pieces: 1, 4 or 16
   float c2;  // scale * log2(e)
 };
 
@@ -73,7 +75,7 @@ struct Cfg {
   static constexpr int kAhead = 2 * (S - 1);       // steps that pages are looked up ahead
   static constexpr int kPages = 256;               // bytes of a wave's pages of one step
   static constexpr int kRing = KW * S * kStage;
-  static constexpr int kJoin = KW > 1 ? (KW - 1) * (D / 2 + 2) * 256 : 0;  // key groups meet in the ring's LDS
+  static constexpr int kJoin = KW > 1 ? KW * (D / 2 + 2) * 256 : 0;  // key groups meet in the ring's LDS
   static_assert(kJoin <= kRing, "LDS of the join");
   static constexpr int kLds = kRing + kWaves * (kAhead + 1) * kPages;
   static constexpr int kMost = D == 64 ? 3 : 2;  // waves that a SIMD's registers hold
@@ -126,14 +128,10 @@ __device__ __forceinline__ uint64_t shfl64(uint64_t x, int src) {
   return ((uint64_t)(uint32_t)__shfl((uint32_t)(x >> 32), src) << 32) | (uint32_t)__shfl((uint32_t)x, src);
 }
 
-// Tiles of a sequence: its cache's, and the tree's.
-template <class C>
-__device__ __forceinline__ int cache_tiles(int len) {
-  return (len + C::kTile - 1) / C::kTile;
-}
+// Tiles of a sequence: its keys are the cache's and right behind them the tree's.
 template <class C>
 __device__ __forceinline__ int seq_tiles(const AttnArgs& a, int b) {
-  return cache_tiles<C>(a.c.len(b)) + (a.T + C::kTile - 1) / C::kTile;
+  return (a.c.len(b) + a.T + C::kTile - 1) / C::kTile;
 }
 
 // a b / c rounded down, for a b < 2^53 and c < 2^32: the quotient is at least 1 / c away from
@@ -193,10 +191,9 @@ __device__ __forceinline__ Where locate(const AttnArgs& a, int* scratch, F want)
   return Where{total, scratch[kThreads], scratch[kThreads + 1]};
 }
 
-// The nodes that node `lane` sees, as bits (none for an unused node): itself and, by
-// doubling along the parents, its ancestors.
-__device__ __forceinline__ uint64_t tree_bits(const int32_t* parents, int T, int lane) {
-  int p = lane < T ? parents[lane] : -2;
+// The nodes that node `lane` (parent p; none: -2) sees, as bits (none for an unused node):
+// itself and, by doubling along the parents, its ancestors.
+__device__ __forceinline__ uint64_t tree_bits(int p, int T, int lane) {
   const bool used = p >= -1 && p < lane;
   uint64_t bits = used ? 1ull << lane : 0;
   if (!used) p = -1;
@@ -220,10 +217,10 @@ struct State {
 };
 
 // Clears the V rows of keys that are not `there`: a weight of zero must not meet what is
-// not finite in them.  With `others` also what is not finite in the rows that are; says
-// whether this lane found any.
+// not finite in them.  In the rows of `nodes` also what is not finite; says whether this lane
+// found any.
 template <class C>
-__device__ __forceinline__ bool clear_rows(char* vt, int rw, int lane, uint64_t there, bool others) {
+__device__ __forceinline__ bool clear_rows(char* vt, int rw, int lane, uint64_t there, uint64_t nodes) {
   bool odd = false;
 #pragma unroll 1
   for (int u = rw * 64 + lane; u < C::kKeys * C::kChunks; u += 64 * C::RW) {
@@ -231,7 +228,7 @@ __device__ __forceinline__ bool clear_rows(char* vt, int rw, int lane, uint64_t 
     uint4* at = reinterpret_cast<uint4*>(vt + row * C::kRowBytes + 16 * (u % C::kChunks));
     if (!((there >> row) & 1)) {
       *at = make_uint4(0, 0, 0, 0);
-    } else if (others) {
+    } else if ((nodes >> row) & 1) {
       uint4 v = *at;
       uint32_t w[4] = {v.x, v.y, v.z, v.w};
       bool here = false;
@@ -375,8 +372,11 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
 
   while (x < x_end) {
     const int len = a.c.len(seq);
-    const int ctiles = cache_tiles<C>(len), tiles = ctiles + (a.T + C::kTile - 1) / C::kTile;
+    const int tiles = (len + a.T + C::kTile - 1) / C::kTile;
     const int first = x - before, last = min(tiles, x_end - before);
+    // for the join: tile y is in part floor(((y + 1) parts - 1) / total)
+    if (a.G > 1 && first == 0 && head == 0 && rt == 0 && threadIdx.x == 0)
+      a.pieces[seq] = make_int2(g, (int)(((double)(before + tiles) * (double)parts - 1.0) / (double)total));
     const int n = last - first;  // steps
     const int32_t* table = a.c.block_table + (int64_t)seq * a.c.table_width;
     // Pages of a step's keys or more: they lie in one, read by a scalar load a step ahead.
@@ -394,47 +394,56 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
     };
     // This wave's share of step i's K and V rows.
     auto load = [&](int i, int wide_id) {
-      const int tile = first + i;
+      const int base = (first + i) * C::kTile + kw * C::kKeys;
       const int rr = lane / C::kChunks, slot = lane % C::kChunks;
       const uint32_t to = ring0 + i % C::S * C::kStage;
       const int* pages = reinterpret_cast<const int*>(my_pages + i % (C::kAhead + 1) * C::kPages);
-      const bool tree = tile >= ctiles;
-      const char* k = tree ? reinterpret_cast<const char*>(a.k_new) : static_cast<const char*>(a.c.k_pages);
-      const char* v = tree ? reinterpret_cast<const char*>(a.v_new) : static_cast<const char*>(a.c.v_pages);
-      if (wide && !tree) {
-        // the step's first key; keys past the end read its page's rows of others, which are masked or cleared
-        const int key = tile * C::kTile + kw * C::kKeys;
+      const char* kp = static_cast<const char*>(a.c.k_pages);
+      const char* vp = static_cast<const char*>(a.c.v_pages);
+      const int in_page = (1 << a.c.page_shift) - 1;
+      if (base + C::kKeys > len) {  // nodes among them, or nothing
+#pragma unroll
+        for (int u = 0; u < C::kLoads; ++u) {
+          int j = rw + C::RW * u;
+          if (C::kLoadsAll % C::RW != 0) j = min(j, C::kLoadsAll - 1);  // the last rows again
+          const int row = j * C::kRowsPerLoad + rr, key = base + row;
+          const int page = min(max(wide ? wide_id : pages[row], 0), a.c.n_pages - 1);
+          const int64_t cached = (int64_t)page * page_bytes +
+                                 (int64_t)((head << a.c.page_shift) + (key & in_page)) * C::kRowBytes;
+          const int64_t node = (((int64_t)seq * a.T + min(key - len, a.T - 1)) * Hkv + head) * C::kRowBytes;
+          const bool tree = key >= len;
+          dma16<C::kOnce>((tree ? reinterpret_cast<const char*>(a.k_new) + node : kp + cached) + 16 * k_slot<C>(slot, row),
+                          __builtin_amdgcn_readfirstlane(to + j * 1024));
+          dma16<C::kOnce>((tree ? reinterpret_cast<const char*>(a.v_new) + node : vp + cached) + 16 * v_slot<C>(slot, row),
+                          __builtin_amdgcn_readfirstlane(to + C::kHalf + j * 1024));
+        }
+        return;
+      }
+      if (wide) {
         const int page = min(max(wide_id, 0), a.c.n_pages - 1);
         const int64_t off = (int64_t)page * page_bytes +
-                            (int64_t)((head << a.c.page_shift) + (key & ((1 << a.c.page_shift) - 1))) * C::kRowBytes;
+                            (int64_t)((head << a.c.page_shift) + (base & in_page)) * C::kRowBytes;
 #pragma unroll
         for (int u = 0; u < C::kLoads; ++u) {
           int j = rw + C::RW * u;
           if (C::kLoadsAll % C::RW != 0) j = min(j, C::kLoadsAll - 1);
           const int row = j * C::kRowsPerLoad + rr;
-          dma16<C::kOnce>(k + off + row * C::kRowBytes + 16 * k_slot<C>(slot, row), __builtin_amdgcn_readfirstlane(to + j * 1024));
-          dma16<C::kOnce>(v + off + row * C::kRowBytes + 16 * v_slot<C>(slot, row),
-                __builtin_amdgcn_readfirstlane(to + C::kHalf + j * 1024));
+          dma16<C::kOnce>(kp + off + row * C::kRowBytes + 16 * k_slot<C>(slot, row), __builtin_amdgcn_readfirstlane(to + j * 1024));
+          dma16<C::kOnce>(vp + off + row * C::kRowBytes + 16 * v_slot<C>(slot, row),
+                          __builtin_amdgcn_readfirstlane(to + C::kHalf + j * 1024));
         }
         return;
       }
 #pragma unroll
       for (int u = 0; u < C::kLoads; ++u) {
         int j = rw + C::RW * u;
-        if (C::kLoadsAll % C::RW != 0) j = min(j, C::kLoadsAll - 1);  // the last rows again
+        if (C::kLoadsAll % C::RW != 0) j = min(j, C::kLoadsAll - 1);
         const int row = j * C::kRowsPerLoad + rr;
-        int64_t off;
-        if (tree) {
-          const int node = min((tile - ctiles) * C::kTile + kw * C::kKeys + row, a.T - 1);
-          off = (((int64_t)seq * a.T + node) * Hkv + head) * C::kRowBytes;
-        } else {
-          const int key = min(tile * C::kTile + kw * C::kKeys + row, len - 1);
-          const int page = min(max(pages[row], 0), a.c.n_pages - 1);
-          off = (int64_t)page * page_bytes +
-                (int64_t)((head << a.c.page_shift) + (key & ((1 << a.c.page_shift) - 1))) * C::kRowBytes;
-        }
-        dma16<C::kOnce>(k + off + 16 * k_slot<C>(slot, row), __builtin_amdgcn_readfirstlane(to + j * 1024));
-        dma16<C::kOnce>(v + off + 16 * v_slot<C>(slot, row), __builtin_amdgcn_readfirstlane(to + C::kHalf + j * 1024));
+        const int page = min(max(pages[row], 0), a.c.n_pages - 1);
+        const int64_t off = (int64_t)page * page_bytes +
+                            (int64_t)((head << a.c.page_shift) + ((base + row) & in_page)) * C::kRowBytes;
+        dma16<C::kOnce>(kp + off + 16 * k_slot<C>(slot, row), __builtin_amdgcn_readfirstlane(to + j * 1024));
+        dma16<C::kOnce>(vp + off + 16 * v_slot<C>(slot, row), __builtin_amdgcn_readfirstlane(to + C::kHalf + j * 1024));
       }
     };
     if (!wide) {
@@ -446,8 +455,8 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
 #pragma unroll
     for (int i = 0; i < C::D / 16; ++i) qf[i] = *reinterpret_cast<const bf16x8*>(a.q + qoff + 16 * i + 8 * h);
     uint64_t sees = 0, used = 0;  // of this lane's row; all used nodes
-    if (last > ctiles) {
-      const uint64_t bits = tree_bits(a.parents + (int64_t)seq * a.T, a.T, lane);
+    if (last == tiles || last * C::kTile > len) {
+      const uint64_t bits = tree_bits(lane < a.T ? a.parents[(int64_t)seq * a.T + lane] : -2, a.T, lane);
       sees = shfl64(bits, t);
       used = __ballot(bits != 0);
     }
@@ -477,21 +486,18 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
       if (i < 0) continue;
       char* kt = const_cast<char*>(ring) + i % C::S * C::kStage;
       char* vt = kt + C::kHalf;
-      const int tile = first + i;
-      const bool tree = tile >= ctiles;
-      const int base = (tree ? tile - ctiles : tile) * C::kTile + kw * C::kKeys;  // first key (or node)
-      const int left = (tree ? a.T : len) - base;                                // that there are from there on
-      bool masked = false;
+      const int base = (first + i) * C::kTile + kw * C::kKeys;  // first key
+      const int cached = len - base, left = cached + a.T;         // of the cache's, of all, from there on
+      const bool masked = cached < C::kKeys;
       uint64_t see = ~0ull;
-      if (tree || left < C::kKeys) {
-        masked = true;
-        uint64_t there = left >= 64 ? ~0ull : left > 0 ? (1ull << left) - 1 : 0;
-        see = there;
-        if (tree) {
-          there = left > 0 ? used >> base : 0;
-          see = left > 0 ? sees >> base : 0;
-        }
-        const bool odd = clear_rows<C>(vt, rw, lane, there, tree);
+      if (masked) {
+        const uint64_t old = cached > 0 ? (1ull << cached) - 1 : 0;  // cached < 64
+        auto placed = [&](uint64_t nodes) {
+          return cached >= 0 ? nodes << cached : left > 0 ? nodes >> -cached : 0;
+        };
+        const uint64_t nodes = placed(used);
+        see = old | placed(sees);
+        const bool odd = clear_rows<C>(vt, rw, lane, old | nodes, nodes);
         if (rw == 0 && lane == 0) s_odd[kw] = 0;
         group_sync<C>();
         if (__ballot(odd) && lane == 0) s_odd[kw] = 1;
@@ -502,11 +508,11 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
         if (left > 32 * sub)
           step<C>((lds_t)kt + sub * 32 * C::kRowBytes, (lds_t)vt + sub * 32 * C::kRowBytes, at, qf, a.c2, lane, masked,
                   (uint32_t)(see >> (32 * sub)), st);
-      if (tree && left > 0 && s_odd[kw]) {
+      if (masked && left > 0 && s_odd[kw]) {
         // what is not finite in a node's V (cleared above) reaches the rows that see the node, and no others
 #pragma unroll 1
-        for (int k = 0; k < min(C::kKeys, left); ++k) {
-          const uint16_t* v = a.v_new + (((int64_t)seq * a.T + base + k) * Hkv + head) * C::D;
+        for (int k = max(cached, 0); k < min(C::kKeys, left); ++k) {
+          const uint16_t* v = a.v_new + (((int64_t)seq * a.T + k - cached) * Hkv + head) * C::D;
           const bool on = (see >> k) & 1;
 #pragma unroll
           for (int dt = 0; dt < C::D / 32; ++dt) {
@@ -522,70 +528,76 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
     }
     __syncthreads();
 
-    // join the key groups
+    // A lane's values in fours, d = 4 h + 8 u of its row.  Key groups: joined through LDS, a
+    // share of the fours to each wave (one wave for all of them: 1.8 us against 0.8 for a
+    // single token).
     const bool whole = first == 0 && last == tiles;
-    st.l += xor32(st.l, lane);
-    if constexpr (C::KW > 1) {
-      float* sh = reinterpret_cast<float*>(lds);
-      constexpr int kSlot = (C::D / 2 + 2) * 64;  // a wave's values
-      if (kw > 0) {
-        float* mine = sh + (wave - C::RW) * kSlot + lane;
+    constexpr int kFours = C::D / 8, kMine = kFours / C::KW;
+    float m = st.m, l = st.l + xor32(st.l, lane);
+    f32x4 o[kMine];
+    if constexpr (C::KW == 1) {
 #pragma unroll
-        for (int dt = 0; dt < C::D / 32; ++dt)
+      for (int u = 0; u < kMine; ++u)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) mine[64 * (16 * dt + i)] = st.o[dt][i];
-        mine[64 * (C::D / 2)] = st.m;
-        mine[64 * (C::D / 2 + 1)] = st.l;
+        for (int e = 0; e < 4; ++e) o[u][e] = st.o[u / 4][4 * (u % 4) + e];
+    } else {
+      static_assert(C::RW == 1, "a wave has all rows");
+      f32x4* sh = reinterpret_cast<f32x4*>(lds) + lane;
+      f32x2* ml = reinterpret_cast<f32x2*>(lds + C::KW * kFours * 1024) + lane;
+      if (row < rows) {
+#pragma unroll
+        for (int u = 0; u < kFours; ++u)
+          sh[64 * (kFours * wave + u)] =
+              f32x4{st.o[u / 4][4 * (u % 4)], st.o[u / 4][4 * (u % 4) + 1], st.o[u / 4][4 * (u % 4) + 2], st.o[u / 4][4 * (u % 4) + 3]};
+        ml[64 * wave] = f32x2{m, l};
       }
       __syncthreads();
-      if (kw == 0) {
-#pragma unroll 1
-        for (int k = 1; k < C::KW; ++k) {
-          const float* other = sh + ((k - 1) * C::RW + rw) * kSlot + lane;
-          const float om = other[64 * (C::D / 2)], ol = other[64 * (C::D / 2 + 1)];
-          const float m = fmaxf(st.m, om);
-          const float f0 = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(st.m - m);
-          const float f1 = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(om - m);
-          st.l = st.l * f0 + ol * f1;
+      if (row < rows) {
+        f32x2 of[C::KW];
+        m = -INFINITY, l = 0.f;
 #pragma unroll
-          for (int dt = 0; dt < C::D / 32; ++dt)
+        for (int k = 0; k < C::KW; ++k) {
+          of[k] = ml[64 * k];
+          m = fmaxf(m, of[k].x);
+        }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) st.o[dt][i] = st.o[dt][i] * f0 + other[64 * (16 * dt + i)] * f1;
-          st.m = m;
+        for (int u = 0; u < kMine; ++u) o[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < C::KW; ++k) {
+          const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(of[k].x - m);
+          l = fmaf(of[k].y, f, l);
+#pragma unroll
+          for (int u = 0; u < kMine; ++u) {
+            const f32x4 v = sh[64 * (kFours * k + kMine * wave + u)];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[u][e] = fmaf(v[e], f, o[u][e]);
+          }
         }
       }
     }
-    if (kw == 0 && row < rows) {
+    if (row < rows) {
+      const int d0 = 8 * kMine * kw + 4 * h;
       if (whole) {
-        const float inv = sees && st.l != 0.f ? 1.0f / st.l : 0.f;
-        uint16_t* o = a.out + qoff;
+        const float inv = sees && l != 0.f ? 1.0f / l : 0.f;
 #pragma unroll
-        for (int dt = 0; dt < C::D / 32; ++dt)
+        for (int u = 0; u < kMine; ++u) {
+          float v[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = inv != 0.f ? st.o[dt][4 * e + i] * inv : 0.f;
-            const bf16x2 lo = __builtin_convertvector(f32x2{v[0], v[1]}, bf16x2);
-            const bf16x2 hi = __builtin_convertvector(f32x2{v[2], v[3]}, bf16x2);
-            union {
-              bf16x2 b[2];
-              uint2 u;
-            } pk;
-            pk.b[0] = lo;
-            pk.b[1] = hi;
-            *reinterpret_cast<uint2*>(o + 32 * dt + 8 * e + 4 * h) = pk.u;
-          }
+          for (int e = 0; e < 4; ++e) v[e] = inv != 0.f ? o[u][e] * inv : 0.f;
+          union {
+            bf16x2 b[2];
+            uint2 u;
+          } pk;
+          pk.b[0] = __builtin_convertvector(f32x2{v[0], v[1]}, bf16x2);
+          pk.b[1] = __builtin_convertvector(f32x2{v[2], v[3]}, bf16x2);
+          *reinterpret_cast<uint2*>(a.out + qoff + d0 + 8 * u) = pk.u;
+        }
       } else {
         const int64_t slot = (slot0 + 2 * g + (first == 0 ? 1 : 0)) * C::kRows + 32 * rw + (lane & 31);
-        float* o = a.part_o + slot * C::D;
 #pragma unroll
-        for (int dt = 0; dt < C::D / 32; ++dt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<f32x4*>(o + 32 * dt + 8 * e + 4 * h) =
-                f32x4{st.o[dt][4 * e], st.o[dt][4 * e + 1], st.o[dt][4 * e + 2], st.o[dt][4 * e + 3]};
-        if (h == 0) *reinterpret_cast<f32x2*>(a.part_ml + 2 * slot) = f32x2{st.m, st.l};
+        for (int u = 0; u < kMine; ++u) *reinterpret_cast<f32x4*>(a.part_o + slot * C::D + d0 + 8 * u) = o[u];
+        if (h == 0 && kw == 0)
+          *reinterpret_cast<f32x2*>(a.part_ml + 2 * slot) = f32x2{m, last == tiles && !sees ? kUnused : l};
       }
     }
     __syncthreads();
@@ -595,111 +607,114 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
   }
 }
 
-// Sequences cut over several workgroups: their pieces joined, 16 (or 4) query rows a
-// workgroup.  16 lanes hold a row's D values.  Few pieces: a row for each 16 lanes; many: a
-// row for a wave, each 16 lanes every fourth piece.  All pieces' loads are independent, so that a row
-// takes a few memory latencies however many pieces it has.
+// Sequences cut over several workgroups: their pieces joined.  16 lanes hold a row's D
+// values and take every `spread`-th of its pieces, two at a time, statistics and values in
+// one go, so that a row takes one memory latency or two however many pieces it has: 16
+// rows a workgroup for few pieces (spread 1), 4 for more (a wave a row), or one.
 template <class C>
 __global__ __launch_bounds__(256) void tree_attention_join_kernel(AttnArgs a) {
   constexpr int kPer = C::D / 16;  // values of a lane
-  __shared__ int scratch[8];
-  const bool many = a.many;
+  constexpr int kAtOnce = 2;       // pieces in flight, per group of lanes
+  __shared__ float tops[4], sums[4][kPer + 1][16];
+  const int spread = a.spread;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int Hkv = a.c.kv_heads, rows = a.T * a.group;
-  const int each = many ? 4 : 16, chunks = (rows + each - 1) / each;
+  const int each = 16 / spread, chunks = (rows + each - 1) / each;
   const int seq = blockIdx.x / (Hkv * chunks), head = blockIdx.x / chunks % Hkv;
   const int row0 = blockIdx.x % chunks * each;
-  // all tiles, and those before this sequence
-  int total, before;
-  if (a.batch == 1) {
-    total = seq_tiles<C>(a, 0), before = 0;
-  } else if (a.batch <= 64) {
-    total = lane < a.batch ? seq_tiles<C>(a, lane) : 0;
-    before = lane < seq ? total : 0;
-#pragma unroll
-    for (int j = 32; j > 0; j >>= 1) {
-      total += (int)xor_lanes((uint32_t)total, j, lane);
-      before += (int)xor_lanes((uint32_t)before, j, lane);
-    }
-  } else {
-    int mine = 0, upto = 0;
-    for (int b = threadIdx.x; b < a.batch; b += 256) {
-      const int n = seq_tiles<C>(a, b);
-      mine += n;
-      if (b < seq) upto += n;
-    }
-    for (int j = 32; j > 0; j >>= 1) {
-      mine += (int)xor_lanes((uint32_t)mine, j, lane);
-      upto += (int)xor_lanes((uint32_t)upto, j, lane);
-    }
-    if (lane == 0) scratch[wave] = mine, scratch[4 + wave] = upto;
-    __syncthreads();
-    total = scratch[0] + scratch[1] + scratch[2] + scratch[3];
-    before = scratch[4] + scratch[5] + scratch[6] + scratch[7];
-  }
-  const int tiles = seq_tiles<C>(a, seq), parts = min(a.G, total);
-  // the first and the last part with a tile of this sequence: tile y is in part
-  // floor(((y + 1) parts - 1) / total)
-  auto part_of = [&](int y) { return uniform((int)(((double)(y + 1) * (double)parts - 1.0) / (double)total)); };
-  const int g0 = part_of(before), g1 = part_of(before + tiles - 1);
+  const int2 at = a.pieces[seq];
+  const int g0 = uniform(at.x), g1 = uniform(at.y);
   if (g0 == g1) return;  // one piece: written already
-  const uint64_t bits = tree_bits(a.parents + (int64_t)seq * a.T, a.T, lane);
-  const int quarter = lane >> 4;
-  {
-    const int row = row0 + (many ? wave : 4 * wave + quarter);
-    const int qrow = min(row, rows - 1), t = qrow / a.group;
-    const bool used = shfl64(bits, t) != 0;
-    const int64_t slot0 = ((int64_t)head * a.row_tiles + qrow / C::kRows) * 2 * a.G;
-    auto slot = [&](int g) { return (slot0 + 2 * g + (g == g0 ? 1 : 0)) * C::kRows + qrow % C::kRows; };
-    float m = -INFINITY;
-    if (many) {
-      for (int g = g0 + lane; g <= g1; g += 64) m = fmaxf(m, a.part_ml[2 * slot(g)]);
+  const int sub = 4 * wave + (lane >> 4);  // of the workgroup's 16 groups of lanes
+  const int row = row0 + sub / spread;
+  const int qrow = min(row, rows - 1), t = qrow / a.group;
+  const int64_t slot0 = ((int64_t)head * a.row_tiles + qrow / C::kRows) * 2 * a.G;
+  const float end = a.part_ml[2 * ((slot0 + 2 * g1) * C::kRows + qrow % C::kRows) + 1];
+  float m = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
-      for (int j = 32; j > 0; j >>= 1) m = fmaxf(m, __uint_as_float(xor_lanes(__float_as_uint(m), j, lane)));
-    } else {
-#pragma unroll 4
-      for (int g = g0; g <= g1; ++g) m = fmaxf(m, a.part_ml[2 * slot(g)]);
+  for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+  for (int g = g0 + sub % spread; g <= g1; g += kAtOnce * spread) {
+    f32x2 ml[kAtOnce];
+    f32x4 v[kAtOnce][kPer / 4];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int gk = min(g + k * spread, g1);
+      const int64_t slot = (slot0 + 2 * gk + (gk == g0 ? 1 : 0)) * C::kRows + qrow % C::kRows;
+      ml[k] = *reinterpret_cast<const f32x2*>(a.part_ml + 2 * slot);
+#pragma unroll
+      for (int e = 0; e < kPer / 4; ++e)
+        v[k][e] = *reinterpret_cast<const f32x4*>(a.part_o + slot * C::D + (lane & 15) * kPer + 4 * e);
     }
-    const float m0 = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[kPer];
+    float top = m;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) o[e] = 0.f;
-#pragma unroll 4
-    for (int g = g0 + (many ? quarter : 0); g <= g1; g += many ? 4 : 1) {
-      const f32x2 ml = *reinterpret_cast<const f32x2*>(a.part_ml + 2 * slot(g));
-      const float* p = a.part_o + slot(g) * C::D + (lane & 15) * kPer;
-      const float f = __builtin_amdgcn_exp2f(ml.x - m0);
-      l += ml.y * f;
+    for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, ml[k].x);  // a piece counted again changes no maximum
+    const float m0 = top == -INFINITY ? 0.f : top;
+    const float was = __builtin_amdgcn_exp2f(m - m0);
+    l *= was;
 #pragma unroll
-      for (int e = 0; e < kPer; e += 4) {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(p + e);
+    for (int e = 0; e < kPer; ++e) o[e] *= was;
 #pragma unroll
-        for (int z = 0; z < 4; ++z) o[e + z] += v[z] * f;
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (g + k * spread <= g1) {
+        const float f = __builtin_amdgcn_exp2f(ml[k].x - m0);
+        l = fmaf(ml[k].y, f, l);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[e] = fmaf(v[k][e / 4][e % 4], f, o[e]);
       }
     }
-    if (many) {
-#pragma unroll
-      for (int j = 16; j <= 32; j += 16) {
-        l += __uint_as_float(xor_lanes(__float_as_uint(l), j, lane));
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) o[e] += __uint_as_float(xor_lanes(__float_as_uint(o[e]), j, lane));
-      }
-    }
-    if (row >= rows || (many && quarter > 0)) return;
-    const bool some = used && l != 0.f;
-    const float inv = some ? 1.0f / l : 0.f;
-    union {
-      bf16x2 b[kPer / 2];
-      uint2 u[kPer / 4];
-    } pk;
-#pragma unroll
-    for (int e = 0; e < kPer; e += 2)
-      pk.b[e / 2] = __builtin_convertvector(some ? f32x2{o[e] * inv, o[e + 1] * inv} : f32x2{0.f, 0.f}, bf16x2);
-    uint16_t* out = a.out + (((int64_t)seq * a.T + t) * Hkv * a.group + head * a.group + row % a.group) * C::D +
-                    (lane & 15) * kPer;
-#pragma unroll
-    for (int e = 0; e < kPer / 4; ++e) reinterpret_cast<uint2*>(out)[e] = pk.u[e];
+    m = top;
   }
+  if (spread > 1) {
+    float top = m;
+#pragma unroll
+    for (int j = 16; j <= 32; j += 16) top = fmaxf(top, __uint_as_float(xor_lanes(__float_as_uint(top), j, lane)));
+    if (spread > 4) {
+      if (lane == 0) tops[wave] = top;
+      __syncthreads();
+      top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+    }
+    const float f = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[e] *= f;
+#pragma unroll
+    for (int j = 16; j <= 32; j += 16) {
+      l += __uint_as_float(xor_lanes(__float_as_uint(l), j, lane));
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] += __uint_as_float(xor_lanes(__float_as_uint(o[e]), j, lane));
+    }
+    if (spread > 4) {
+      if (lane < 16) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) sums[wave][e][lane] = o[e];
+        sums[wave][kPer][lane] = l;
+      }
+      __syncthreads();
+      l = 0.f;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        l += sums[w][kPer][lane & 15];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[e] += sums[w][e][lane & 15];
+      }
+    }
+  }
+  if (row >= rows || sub % spread > 0) return;
+  const bool some = end != kUnused && l != 0.f;
+  const float inv = some ? 1.0f / l : 0.f;
+  union {
+    bf16x2 b[kPer / 2];
+    uint2 u[kPer / 4];
+  } pk;
+#pragma unroll
+  for (int e = 0; e < kPer; e += 2)
+    pk.b[e / 2] = __builtin_convertvector(some ? f32x2{o[e] * inv, o[e + 1] * inv} : f32x2{0.f, 0.f}, bf16x2);
+  uint16_t* out = a.out + (((int64_t)seq * a.T + t) * Hkv * a.group + head * a.group + row % a.group) * C::D +
+                  (lane & 15) * kPer;
+#pragma unroll
+  for (int e = 0; e < kPer / 4; ++e) reinterpret_cast<uint2*>(out)[e] = pk.u[e];
 }
 
 template <class C>
@@ -708,7 +723,7 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.G == 1) return e;
   tree_attention_join_kernel<C><<<
-      dim3((uint32_t)(a.batch * a.c.kv_heads * cdiv(a.T * a.group, a.many ? 4 : 16))), dim3(256), 0, stream>>>(a);
+      dim3((uint32_t)(a.batch * a.c.kv_heads * cdiv(a.T * a.group, 16 / a.spread))), dim3(256), 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -734,12 +749,13 @@ AttnPlan plan_tree_attention(const CacheView& c, int64_t batch, int64_t T, int64
     p.row_tiles = cdiv(rows, C::kRows);
     // tiles when all lengths are full: no more parts than that
     const int64_t most =
-        batch * (cdiv((int64_t)c.table_width << c.page_shift, C::kTile) + cdiv(T, (int64_t)C::kTile));
+        batch * cdiv(((int64_t)c.table_width << c.page_shift) + T, (int64_t)C::kTile);
     p.G = 256 * C::kGroups / (p.row_tiles * c.kv_heads);
     p.G = p.G < 1 ? 1 : p.G > most ? most : p.G;
     const int64_t slots = (int64_t)c.kv_heads * p.row_tiles * 2 * p.G * C::kRows;
     p.part_bytes = p.G > 1 ? align_up((size_t)(slots * D) * 4, 256) : 0;
-    p.ws_bytes = p.G > 1 ? p.part_bytes + align_up((size_t)slots * 8, 256) : 0;
+    p.ml_bytes = p.G > 1 ? align_up((size_t)slots * 8, 256) : 0;
+    p.ws_bytes = p.G > 1 ? p.part_bytes + p.ml_bytes + align_up((size_t)batch * 8, 256) : 0;
     return p;
   };
   return D == 64 ? with_cfg<64>(rows, plan) : with_cfg<128>(rows, plan);
@@ -757,12 +773,13 @@ hipError_t launch_tree_attention(const AttnPlan& p, const CacheView& c, const vo
   a.out = static_cast<uint16_t*>(out);
   a.part_o = static_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_bytes);
+  a.pieces = reinterpret_cast<int2*>(static_cast<char*>(ws) + p.part_bytes + p.ml_bytes);
   a.batch = (int)batch;
   a.T = (int)T;
   a.group = (int)group;
   a.G = (int)p.G;
   a.row_tiles = (int)p.row_tiles;
-  a.many = p.G >= 8 * batch;
+  a.spread = p.G >= 32 * batch ? 16 : p.G >= 8 * batch ? 4 : 1;  // by its pieces
   a.c2 = (float)(scale * 1.4426950408889634);
   auto run = [&](auto cfg) { return launch<decltype(cfg)>(a, stream); };
   return D == 64 ? with_cfg<64>(T * group, run) : with_cfg<128>(T * group, run);

@@ -225,7 +225,8 @@ hipError_t launch_cache_commit(const CacheView& c, const void* k_new, const void
 struct AttnPlan {
   int64_t row_tiles;       // workgroups for a head's rows
   int64_t G;               // parts that the keys of a head are cut into
-  size_t part_bytes;       // of the parts' fp32 sums; their maxima and sums follow
+  size_t part_bytes;       // of the parts' fp32 sums,
+  size_t ml_bytes;         // of their maxima and sums; each sequence's parts follow
   size_t ws_bytes;
 };
 AttnPlan plan_tree_attention(const CacheView& c, int64_t batch, int64_t T, int64_t group, int64_t D);
