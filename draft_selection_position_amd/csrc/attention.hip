@@ -81,6 +81,10 @@ struct Cfg {
   static constexpr int kMost = D == 64 ? 3 : 2;  // waves that a SIMD's registers hold
   static constexpr int kByLds = 163840 / (kLds + 2304), kByWaves = 4 * kMost / kWaves;
   static constexpr int kGroups = kByLds < kByWaves ? kByLds : kByWaves;  // workgroups of a CU
+  // Three waves of a SIMD: the oldest is served first and the last ends far behind (95, 106 and
+  // 128 us), alone on its SIMD.  A wave gives way as it gets on: 147.3 -> 142.8 us at 2 x 64
+  // nodes x 131001 keys; with two waves it gains nothing.
+  static constexpr bool kEven = kGroups * kWaves > 8;
   static constexpr int kMinWaves = kGroups * kWaves > 8 ? 3 : kGroups * kWaves > 4 ? 2 : 1;  // per SIMD
 };
 
@@ -260,27 +264,36 @@ struct Frag {
   }
 };
 
-// A step's 32 keys: scores, weights, sums.  `masked`: only the keys whose bit is set in
-// this lane's `sees` count.
+// A step's keys: scores, weights, sums.  `masked`: only the keys whose bit is set in this
+// lane's `sees` count.  Its tiles of 32 keys go side by side, so that one's matrix products
+// run under the other's exponentials.
 template <class C>
 __device__ __forceinline__ void step(lds_t kt, lds_t vt, const Frag<C>& at, const bf16x8 (&qf)[C::D / 16], float c2,
-                                     int lane, bool masked, uint32_t sees, State<C>& st) {
+                                     int lane, bool masked, uint64_t sees, State<C>& st) {
   typedef __attribute__((address_space(3))) const bf16x8* k_ptr;
   typedef __attribute__((address_space(3))) s16x4* tr_ptr;
-  f32x16 s = {};
+  constexpr int kSub = 32 * C::kRowBytes;  // bytes of 32 keys
+  f32x16 s[C::SUB];
 #pragma unroll
-  for (int x = 0; x < C::D / 16; ++x) {
-    const bf16x8 kf = *(k_ptr)(kt + (at.k ^ (32 * x)));
-    s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[x], s, 0, 0, 0);
+  for (int sub = 0; sub < C::SUB; ++sub) {
+    s[sub] = f32x16{};
+#pragma unroll
+    for (int x = 0; x < C::D / 16; ++x) {
+      const bf16x8 kf = *(k_ptr)(kt + sub * kSub + (at.k ^ (32 * x)));
+      s[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[x], s[sub], 0, 0, 0);
+    }
   }
   if (masked) {
-    const uint32_t bits = sees >> (4 * (lane >> 5));
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = (bits >> (8 * (i / 4) + i % 4)) & 1 ? s[i] : -INFINITY;
+    for (int sub = 0; sub < C::SUB; ++sub) {
+      const uint32_t bits = (uint32_t)(sees >> (32 * sub)) >> (4 * (lane >> 5));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[sub][i] = (bits >> (8 * (i / 4) + i % 4)) & 1 ? s[sub][i] : -INFINITY;
+    }
   }
-  float top = s[0];
+  float top = s[0][0];
 #pragma unroll
-  for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+  for (int i = 1; i < 16 * C::SUB; ++i) top = fmaxf(top, s[i / 16][i % 16]);
   top = fmaxf(top, xor32(top, lane)) * c2;
   // A row's maximum follows only when it lags by more than 2^8: weights are then at most
   // 2^8 and nothing is lost, and most steps leave the sums alone.
@@ -295,32 +308,37 @@ __device__ __forceinline__ void step(lds_t kt, lds_t vt, const Frag<C>& at, cons
     st.m = m;
   }
   const float m0 = st.m == -INFINITY ? 0.f : st.m;
-  float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c2, -m0));
-    sum += s[i];
-  }
-  st.l += sum;
+  for (int sub = 0; sub < C::SUB; ++sub) {
+    float sum = 0.f;
 #pragma unroll
-  for (int kc = 0; kc < 2; ++kc) {
-    union {
-      bf16x2 two[4];
-      bf16x8 all;
-    } pf;
+    for (int i = 0; i < 16; ++i) {
+      s[sub][i] = __builtin_amdgcn_exp2f(fmaf(s[sub][i], c2, -m0));
+      sum += s[sub][i];
+    }
+    st.l += sum;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      pf.two[i] = __builtin_convertvector(f32x2{s[8 * kc + 2 * i], s[8 * kc + 2 * i + 1]}, bf16x2);
-#pragma unroll
-    for (int dt = 0; dt < C::D / 32; ++dt) {
+    for (int kc = 0; kc < 2; ++kc) {
       union {
-        s16x4 half[2];
+        bf16x2 two[4];
         bf16x8 all;
-      } vf;
+      } pf;
 #pragma unroll
-      for (int z = 0; z < 2; ++z)
-        vf.half[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)(vt + at.v[dt] + (16 * kc + 8 * z) * C::kRowBytes));
-      st.o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf.all, pf.all, st.o[dt], 0, 0, 0);
+      for (int i = 0; i < 4; ++i) {
+        pf.two[i] = __builtin_convertvector(f32x2{s[sub][8 * kc + 2 * i], s[sub][8 * kc + 2 * i + 1]}, bf16x2);
+      }
+#pragma unroll
+      for (int dt = 0; dt < C::D / 32; ++dt) {
+        union {
+          s16x4 half[2];
+          bf16x8 all;
+        } vf;
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+          vf.half[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (tr_ptr)(vt + sub * kSub + at.v[dt] + (16 * kc + 8 * z) * C::kRowBytes));
+        st.o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf.all, pf.all, st.o[dt], 0, 0, 0);
+      }
     }
   }
 }
@@ -356,7 +374,8 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
   const int total = uniform(w.total), parts = min(a.G, total);
   if (g >= parts) return;
   int x = uniform(mul_div(g, total, parts));
-  const int x_end = uniform(mul_div(g + 1, total, parts));
+  const int x_end = uniform(mul_div(g + 1, total, parts)), steps = x_end - x;
+  if constexpr (C::kEven) __builtin_amdgcn_s_setprio(3);
   const int rows = a.T * a.group;
   const int row = rt * C::kRows + 32 * rw + (lane & 31);
   const int qrow = min(row, rows - 1), t = qrow / a.group, gh = qrow % a.group;
@@ -484,6 +503,12 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
         if (wide) next_page = wide_page(i + C::S);
       }
       if (i < 0) continue;
+      if constexpr (C::kEven) {
+        const int rest = x_end - (before + first + i);
+        if (rest == steps / 2) __builtin_amdgcn_s_setprio(2);
+        if (rest == steps / 4) __builtin_amdgcn_s_setprio(1);
+        if (rest == steps / 8) __builtin_amdgcn_s_setprio(0);
+      }
       char* kt = const_cast<char*>(ring) + i % C::S * C::kStage;
       char* vt = kt + C::kHalf;
       const int base = (first + i) * C::kTile + kw * C::kKeys;  // first key
@@ -503,11 +528,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
         if (__ballot(odd) && lane == 0) s_odd[kw] = 1;
         group_sync<C>();
       }
-#pragma unroll
-      for (int sub = 0; sub < C::SUB; ++sub)
-        if (left > 32 * sub)
-          step<C>((lds_t)kt + sub * 32 * C::kRowBytes, (lds_t)vt + sub * 32 * C::kRowBytes, at, qf, a.c2, lane, masked,
-                  (uint32_t)(see >> (32 * sub)), st);
+      if (left > 0) step<C>((lds_t)kt, (lds_t)vt, at, qf, a.c2, lane, masked, see, st);
       if (masked && left > 0 && s_odd[kw]) {
         // what is not finite in a node's V (cleared above) reaches the rows that see the node, and no others
 #pragma unroll 1
