@@ -114,11 +114,12 @@ __device__ __forceinline__ void store4(void* out, int64_t row, int64_t N, int64_
   }
 }
 
-// WN x WR waves, each TN x TR tiles of 16 columns (of w) x 16 rows (of a).
-template <int WN_, int WR_, int TN_, int TR_, int S_>
+// WN x WR waves, each TN x TR tiles of 16 columns (of w) x 16 rows (of a); KG such groups, each
+// with a ring of S stages of its own, take the blocks of k in turn.
+template <int WN_, int WR_, int TN_, int TR_, int S_, int KG_ = 1>
 struct Tile {
-  static constexpr int WN = WN_, WR = WR_, TN = TN_, TR = TR_, S = S_;
-  static constexpr int kWaves = WN * WR, kThreads = 64 * kWaves;
+  static constexpr int WN = WN_, WR = WR_, TN = TN_, TR = TR_, S = S_, KG = KG_;
+  static constexpr int kWaves = WN * WR, kThreads = 64 * kWaves * KG;  // waves of a group
   static constexpr int BN = 16 * TN * WN, BR = 16 * TR * WR;
   static_assert(kBlock % (16 * TN) == 0, "a wave's columns share a scale");
   static constexpr int kScaleLoads = BR / 64;  // 64 rows' scales a load
@@ -128,8 +129,9 @@ struct Tile {
   static constexpr int kPerStep = kLoads + 1;  // loads of a wave per step, the scales' among them
   static constexpr int kScales = (BN + BR) * kBlock;        // a's scales in a stage, w's after them
   static constexpr int kStage = kScales + 4 * BR + 256;
-  static constexpr int kLds = S * kStage;
-  static constexpr int kMinWaves = kWaves == 8 ? 2 : 1;  // per SIMD
+  static constexpr int kLds = KG * S * kStage;
+  static_assert((KG - 1) * BN * BR * 4 <= kLds, "the groups' sums meet in the ring's LDS");
+  static constexpr int kMinWaves = kWaves * KG / 4;  // per SIMD
 };
 
 __device__ __forceinline__ void dma4(big::rsrc_t rsrc, uint32_t voff, uint32_t lds_base) {
@@ -211,7 +213,7 @@ template <class C, bool kBf16>
 __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void linear_q8_tile_kernel(LinearArgs p) {
   __shared__ __align__(1024) char lds[C::kLds];
   const int lane = threadIdx.x & 63;
-  const int wave = uniform(threadIdx.x >> 6);
+  const int kg = uniform(threadIdx.x >> 6) / C::kWaves, wave = uniform(threadIdx.x >> 6) % C::kWaves;
   const int r = lane & 15, g = lane >> 4;
   const int wn = wave / C::WR, wr = wave % C::WR;
   const int2 at = tile_of(blockIdx.x, gridDim.x, (int)((p.rows + C::BR - 1) / C::BR), (int)((p.N + C::BN - 1) / C::BN));
@@ -242,23 +244,25 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void linear_q8_tile_kern
   for (int i = 0; i < C::TN; ++i)
 #pragma unroll
     for (int j = 0; j < C::TR; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int n = p.G;
-  const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((big::lds_ptr_t)lds);
+  const int n = p.G, steps = (n + C::KG - 1) / C::KG;  // this group's: blocks kg, kg + KG, ...
+  const char* ring = lds + kg * C::S * C::kStage;
+  const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((big::lds_ptr_t)lds) + kg * C::S * C::kStage;
 #pragma unroll
   for (int j = 0; j < C::S - 1; ++j) {
 #pragma unroll
-    for (int i = 0; i < C::kLoads; ++i) in.one(lds0 + j * C::kStage, min(j, n - 1), i);
-    in.scale(lds0 + j * C::kStage, min(j, n - 1));
+    for (int i = 0; i < C::kLoads; ++i) in.one(lds0 + j * C::kStage, min(j * C::KG + kg, n - 1), i);
+    in.scale(lds0 + j * C::kStage, min(j * C::KG + kg, n - 1));
   }
   constexpr bool kExact = !kBf16;
   typedef Operand<kExact> Op;
   constexpr int kSpread = (C::kLoads + C::TN - 1) / C::TN;  // loads issued per column tile
-  for (int ks = 0; ks < n; ++ks) {
+  for (int ks = 0; ks < steps; ++ks) {
     big::wait_vmcnt<(C::S - 2) * C::kPerStep>();
     big::bar();
-    const int nxt = ks + C::S - 1;  // past the end: the last step again
-    const uint32_t fill = lds0 + (nxt % C::S) * C::kStage;
-    const char* st = lds + (ks % C::S) * C::kStage;
+    if (C::KG > 1 && ks * C::KG + kg >= n) break;  // in the last step, which nothing follows
+    const int nxt = min((ks + C::S - 1) * C::KG + kg, n - 1);  // past the end: the last block again
+    const uint32_t fill = lds0 + (ks + C::S - 1) % C::S * C::kStage;
+    const char* st = ring + (ks % C::S) * C::kStage;
     Op fa[C::TR];
     float sc[C::TR];
     // A column tile's products while the one before is added up, the next one's fragment is
@@ -287,8 +291,8 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void linear_q8_tile_kern
         if (j == 0) {
           if (i + 2 < C::TN) fw[(i + 2) % 3] = Op(read_frag(wt + 16 * (i + 2) * kBlock, r, g));
 #pragma unroll
-          for (int x = i * kSpread; x < min((i + 1) * kSpread, C::kLoads); ++x) in.one(fill, min(nxt, n - 1), x);
-          if (i == C::TN - 1) in.scale(fill, min(nxt, n - 1));
+          for (int x = i * kSpread; x < min((i + 1) * kSpread, C::kLoads); ++x) in.one(fill, nxt, x);
+          if (i == C::TN - 1) in.scale(fill, nxt);
         }
         if (i == 0) sc[j] *= ws;
         if (i > 0) add_scaled(acc[i - 1][j], t[(i - 1) & 1][j], sc[j]);
@@ -300,6 +304,25 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void linear_q8_tile_kern
   }
   big::wait_vmcnt<0>();
   big::bar();  // everyone is done with the ring
+  if constexpr (C::KG > 1) {  // the groups' sums, in their order
+    f32x4* sums = reinterpret_cast<f32x4*>(lds) + wave * C::TN * C::TR * 64 + lane;
+    constexpr int kOne = C::kWaves * C::TN * C::TR * 64;
+    if (kg > 0)
+#pragma unroll
+      for (int i = 0; i < C::TN; ++i)
+#pragma unroll
+        for (int j = 0; j < C::TR; ++j) sums[(kg - 1) * kOne + (i * C::TR + j) * 64] = acc[i][j];
+    __syncthreads();
+    if (kg == 0)
+#pragma unroll
+      for (int k = 1; k < C::KG; ++k)
+#pragma unroll
+        for (int i = 0; i < C::TN; ++i)
+#pragma unroll
+          for (int j = 0; j < C::TR; ++j) acc[i][j] += sums[(k - 1) * kOne + (i * C::TR + j) * 64];
+    __syncthreads();
+    if (kg > 0) return;
+  }
   // A wave's tile goes out by way of LDS, 16 rows at a time, so that a row's columns leave as
   // one run (a lane holds 4 columns of a row: written from there they went out in 32-byte
   // pieces, which took 10% of the kernel at 4096 x 151936 x 5120).
@@ -348,10 +371,12 @@ hipError_t launch_tile(const LinearArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-using Big = Tile<2, 4, 8, 4, 2>;    // 256 x 256, one workgroup a CU
-using Mid = Tile<2, 2, 4, 4, 2>;    // 128 x 128, two
-using Small = Tile<2, 2, 2, 2, 3>;  // 64 x 64, three
-using Wide = Tile<4, 1, 2, 4, 3>;   // 128 columns x 64 rows, two
+using Big = Tile<2, 4, 8, 4, 2>;      // 256 x 256, one workgroup a CU
+using Mid = Tile<2, 2, 4, 4, 2>;      // 128 x 128, two
+using Tall = Tile<4, 2, 2, 2, 3>;     // 128 columns x 64 rows, two
+using Small = Tile<2, 2, 2, 2, 3>;    // 64 x 64, three
+using Pair = Tile<2, 2, 2, 2, 4, 2>;  // 64 x 64 by two groups of waves, one
+using Wide = Tile<4, 1, 2, 4, 3>;     // 128 columns x 64 rows, two
 
 // Few rows: the time is that of reading w once.  No LDS ring: a workgroup's eight waves
 // take the blocks of k in turn, each reads NB blocks' fragments of w (16 rows x 128 bytes:
@@ -576,11 +601,15 @@ hipError_t launch_stream(const LinearArgs& p, hipStream_t stream) {
 //                  fp32: 148 against 182), else the one for few rows (1 x 5120 x 4096: 6.6)
 //   up to 32 rows  the same, the streaming one up to 24 blocks of k (its fragments of a spill beyond)
 //   up to 64 rows  128 x 64 tiles from 16384 columns on (64 x 60000 x 4096: 58 against 108), else the
-//                  kernel for few rows up to 48 (48 x 5120 x 4096: 11.8), 64 x 64 tiles beyond
+//                  kernel for few rows up to 48 (48 x 5120 x 4096: 11.8), then as for more
 //   more           256 x 256 tiles if there are four rounds of them (4096 x 151936 x 5120: 3055
 //                  against 4052 in 128 x 128), 128 x 128 from 300 on (1024 x 10240 x 5120: 89 against
-//                  111 in 64 x 64), else 64 x 64 (333 x 5003 x 2064: 15 against 22).  With an fp32
-//                  output the 256 x 256 tile spills, and 128 x 128 takes its place.
+//                  111 in 64 x 64), else 64 x 64: one for each CU or less, and two groups of waves
+//                  take the blocks of k in turn (192 x 5120 x 5120: 13.5 against 17.5); two for each
+//                  or less, and one workgroup of eight waves takes two of them (333 x 5003 x 2064:
+//                  12.9 against 14.0; 512 x 5120 x 4096, 640 tiles: 26.6 against 23.9).  With an
+//                  fp32 output (twice the matrix instructions) the latter gains nothing, and the
+//                  256 x 256 tile spills: 128 x 128 takes its place.
 template <bool kBf16>
 hipError_t launch_linear(const LinearArgs& p, hipStream_t stream) {
   const bool columns = p.N >= 16384;
@@ -595,6 +624,10 @@ hipError_t launch_linear(const LinearArgs& p, hipStream_t stream) {
   if constexpr (kBf16)
     if (cdiv(p.rows, Big::BR) * cdiv(p.N, Big::BN) >= 1024) return launch_tile<Big, kBf16>(p, stream);
   if (cdiv(p.rows, Mid::BR) * cdiv(p.N, Mid::BN) >= 300) return launch_tile<Mid, kBf16>(p, stream);
+  const int64_t tiles = cdiv(p.rows, Small::BR) * cdiv(p.N, Small::BN);
+  if (tiles <= 256) return launch_tile<Pair, kBf16>(p, stream);
+  if constexpr (kBf16)
+    if (tiles <= 512) return launch_tile<Tall, kBf16>(p, stream);
   return launch_tile<Small, kBf16>(p, stream);
 }
 

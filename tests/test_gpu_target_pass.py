@@ -173,6 +173,13 @@ def test_linear_many_rows(dfs, rows, N, K):
     check_linear(dfs, gen(N + 1), rows, N, K, torch.float32)
 
 
+@pytest.mark.parametrize("rows,N,K", [(333, 5003, 2064), (700, 2001, 144), (1030, 1900, 1296), (65, 16300, 16)])
+def test_linear_middling_rows(dfs, rows, N, K):
+    """More 64 x 64 tiles than CUs, up to twice as many: workgroups of eight waves."""
+    check_linear(dfs, gen(rows + K), rows, N, K, torch.bfloat16)
+    check_linear(dfs, gen(rows - K), rows, N, K, torch.float32)
+
+
 def test_linear_values_that_are_not_finite(dfs):
     """A NaN or an infinite scale reaches its own row or column only (the matrix core reads whole tiles)."""
     g = gen(3)
