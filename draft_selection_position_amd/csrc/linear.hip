@@ -255,7 +255,11 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void linear_q8_tile_kern
   }
   constexpr bool kExact = !kBf16;
   typedef Operand<kExact> Op;
-  constexpr int kSpread = (C::kLoads + C::TN - 1) / C::TN;  // loads issued per column tile
+  // Loads issued per column tile.  With two stages they are due at the step's end: twice as many, and
+  // so all of them in its first half (4096 x 151936 x 5120: 3005 -> 2944 us; with more stages the
+  // even spread is better, 192 x 5120 x 5120: 13.5 against 14.7).
+  constexpr bool kSoon = C::S == 2;
+  constexpr int kSpread = (kSoon ? 2 : 1) * ((C::kLoads + C::TN - 1) / C::TN);
   for (int ks = 0; ks < steps; ++ks) {
     big::wait_vmcnt<(C::S - 2) * C::kPerStep>();
     big::bar();
@@ -292,7 +296,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void linear_q8_tile_kern
           if (i + 2 < C::TN) fw[(i + 2) % 3] = Op(read_frag(wt + 16 * (i + 2) * kBlock, r, g));
 #pragma unroll
           for (int x = i * kSpread; x < min((i + 1) * kSpread, C::kLoads); ++x) in.one(fill, nxt, x);
-          if (i == C::TN - 1) in.scale(fill, nxt);
+          if (i == (kSoon ? 0 : C::TN - 1)) in.scale(fill, nxt);
         }
         if (i == 0) sc[j] *= ws;
         if (i > 0) add_scaled(acc[i - 1][j], t[(i - 1) & 1][j], sc[j]);
