@@ -7,9 +7,12 @@
 // the sum of squares is reduced over its waves, and a group's 128 values are 16
 // neighbouring lanes, so its largest value is four DPP steps.  s stays in fp32 from the
 // addition to the quantisation: the rounded sum that later layers read (out_total) is not
-// what is normalised.  The quotient y / scale is taken as y (1 / scale): off by at most
-// three fp32 roundings, which can move a value that lies that close to the border of two
-// e4m3 steps to the other one.
+// what is normalised.
+//
+// The quotient.  1 / sqrt(...) is common to a group, so y / scale = 448 s w / max|s w|: taken in
+// 64 bits, where s w is exact, and rounded to e4m3 once (by way of 20 bits with a sticky last
+// one).  In fp32 its four or five roundings moved a few of a million values, those that lie
+// next to the border of two e4m3 steps, to the other step.
 #include "dfs_device.h"
 #include "dfs_internal.h"
 
@@ -51,19 +54,16 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[kVec]
   }
 }
 
-// fp32 -> bf16 bits, round to nearest, ties to even; NaN stays NaN.
-__device__ __forceinline__ uint32_t bf16_bits(float f) {
-  const uint32_t u = __float_as_uint(f);
-  return f != f ? 0x7fc0u : (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
-}
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 template <bool kBf16>
 __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[kVec]) {
   if constexpr (kBf16) {
-    uint32_t w[4];
+    f32x8 f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = bf16_bits(v[2 * j]) | (bf16_bits(v[2 * j + 1]) << 16);
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int j = 0; j < kVec; ++j) f[j] = v[j];
+    *reinterpret_cast<bf16x8*>(static_cast<uint16_t*>(p) + i) = __builtin_convertvector(f, bf16x8);  // to nearest, ties to even
   } else {
     float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
     f[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -78,6 +78,26 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t x) {
   x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x122, 0xF, 0xF, false));  // row_ror:2
   x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x121, 0xF, 0xF, false));  // row_ror:1
   return x;
+}
+
+// The same of doubles that are not negative: they compare as whole numbers.
+template <int kCtrl>
+__device__ __forceinline__ double max_ror(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)u, kCtrl, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), kCtrl, 0xF, 0xF, false);
+  return fmax(x, __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo));
+}
+__device__ __forceinline__ double row16_max(double x) {
+  return max_ror<0x121>(max_ror<0x122>(max_ror<0x124>(max_ror<0x128>(x))));
+}
+
+// To fp32 with the last of 20 bits odd where something was cut off: what is then rounded to
+// fewer bits is rounded as the double would have been.
+__device__ __forceinline__ float sticky20(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t hi = (uint32_t)(u >> 32) | ((uint32_t)u != 0 ? 1u : 0u);
+  return (float)__builtin_bit_cast(double, (uint64_t)hi << 32);
 }
 
 __device__ __forceinline__ float wave_sum(float v, int lane) {
@@ -132,13 +152,19 @@ __global__ __launch_bounds__(kWaves == 1 ? 4 * kWave : kWaves* kWave) void norm_
     const int c = (i * kWaves + part) * kStep + lane * kVec;
     const bool in = c < a.d;
     float y[kVec];
+    double p[kVec];  // s w
     uint32_t most = 0;
+    double pmost = 0.0;
     if (in) {
       if (kRes && a.total) store8<kBf16>(a.total, base + c, s[i]);
       float w[kVec];
       load8<kBf16>(a.weight, c, w);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) y[j] = s[i][j] * inv * w[j];
+      for (int j = 0; j < kVec; ++j) {
+        y[j] = s[i][j] * inv * w[j];
+        p[j] = (double)s[i][j] * (double)w[j];
+        pmost = fmax(pmost, fabs(p[j]));
+      }
       if (a.normed) store8<kBf16>(a.normed, base + c, y);
       // magnitudes as integers: order-preserving, and a NaN is the largest of all
 #pragma unroll
@@ -146,13 +172,24 @@ __global__ __launch_bounds__(kWaves == 1 ? 4 * kWave : kWaves* kWave) void norm_
     }
     const float top = __uint_as_float(row16_max(most));
     const float scale = top != top ? top : fmaxf(top / kE4m3Max, 0x1p-100f);
+    pmost = row16_max(pmost);
     if (in) {
-      const float mul = 1.0f / scale;
+      // 448 / pmost to about 2^-50: far more than what is left of it
+      double k = __builtin_amdgcn_rcp(pmost);
+      k = fma(fma(-pmost, k, 1.0), k, k);
+      k = scale > 0x1p-100f ? fma(fma(-pmost, k, 1.0), k, k) * (double)kE4m3Max : (double)inv * 0x1p100;
+      if (top < INFINITY) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) y[j] = sticky20(p[j] * k);
+      } else {  // over an infinite scale: 0 or, where y is not finite itself, NaN
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) y[j] *= top != top ? NAN : 0.f;
+      }
       int w0 = 0, w1 = 0;
-      w0 = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] * mul, y[1] * mul, w0, false);
-      w0 = __builtin_amdgcn_cvt_pk_fp8_f32(y[2] * mul, y[3] * mul, w0, true);
-      w1 = __builtin_amdgcn_cvt_pk_fp8_f32(y[4] * mul, y[5] * mul, w1, false);
-      w1 = __builtin_amdgcn_cvt_pk_fp8_f32(y[6] * mul, y[7] * mul, w1, true);
+      w0 = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], w0, false);
+      w0 = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w0, true);
+      w1 = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], w1, false);
+      w1 = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], w1, true);
       *reinterpret_cast<int2*>(a.q + base + c) = make_int2(w0, w1);
       if ((lane & 15) == 0) a.scale[(int64_t)(c >> 7) * a.rows + row] = scale;
     }
