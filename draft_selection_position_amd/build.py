@@ -30,8 +30,8 @@ COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-Wno-unused-result",
 
 # Of single sources: matrix products with their sums in ordinary registers, where vector
 # instructions use them next.  The compiler would keep some in accumulation registers and copy
-# them back and forth (attention for few rows: 750 copies, 17.8 us against 15.1 for one token;
-# the 8-bit product in 128 x 128 tiles: 88 us against 84).
+# them back and forth (attention of one token: 12.1 us against 11.8; the 8-bit product in
+# 128 x 128 tiles, 1024 x 10240 x 5120: 88 against 84).
 _SUMS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 SOURCE_FLAGS = {"attention.hip": _SUMS, "linear.hip": _SUMS}
 

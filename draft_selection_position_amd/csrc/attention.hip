@@ -11,17 +11,23 @@
 // 32 away, a rescale is one factor per lane, and P^T's registers are already the second
 // product's operand (its 16 keys per instruction are taken in the order in which S^T's
 // sums lie; V^T comes out of LDS in the same order by the transposing read).  P is rounded
-// to bf16 for the matrix cores (relative 2^-9 per weight, as the output's own rounding);
+// to bf16 for the matrix cores (relative 2^-8 per weight, as the output's own rounding);
 // scores, maxima, sums and O stay in fp32.
 //
-// K and V tiles of 32 keys go from memory straight into LDS, through a ring of stages.  Few
-// query rows: four waves take tiles of their own and never wait for each other until they
-// are joined at the end.  More rows: the waves of a workgroup share a tile, 32 rows each.
+// K and V tiles go from memory straight into LDS, through a ring of stages.  Up to 32 query
+// rows: four waves take tiles of 32 keys of their own and never wait for each other until they
+// are joined at the end.  More rows: the waves of a workgroup share a tile of 64, 32 rows each.
 // Pages are looked up two ring lengths ahead, through LDS as well: a load into a register
 // in the loop would make the compiler wait for everything in flight.  Work is split along
 // the keys: the tiles of all sequences in a row are cut evenly over the workgroups of a
 // head, whatever the lengths are; sequences that were cut are joined by a second kernel
-// from fp32 partial results.
+// from fp32 partial results.  A sequence's nodes are keys like the cache's, right behind them.
+//
+// What bounds it (MI355X): 64 sequences of 17 nodes, 4 heads to a kv head of 128, 0 to 8192 cached
+// keys: 205 us, memory at 5.3 TB/s.  2 x 64 nodes x 6 heads to a kv head of 64, 131001 keys: 142 to
+// 148 us, 700 TFLOP/s; a head of 64 costs as many exponentials as products' cycles, and the
+// card holds 2.0 GHz under it.  One token, 4001 keys: 11.8 us, two launches and a chain of four
+// memory latencies (lengths, pages, keys, pieces); its 16 MB would take 2.5.
 #include "dfs_device.h"
 #include "dfs_internal.h"
 #include "mfma_big.h"
@@ -89,7 +95,7 @@ struct Cfg {
 };
 
 // 16 bytes per lane from memory straight into LDS at lds_base + 16 lane; kOnce: nobody else
-// reads them (64 sequences x 17 nodes, 8192 keys: 232 us against 254 without the hint).
+// reads them (64 sequences x 17 nodes, 8192 keys: 203 us against 221 without the hint).
 template <bool kOnce>
 __device__ __forceinline__ void dma16(const void* p, uint32_t lds_base) {
   if constexpr (kOnce)
@@ -550,7 +556,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
     __syncthreads();
 
     // A lane's values in fours, d = 4 h + 8 u of its row.  Key groups: joined through LDS, a
-    // share of the fours to each wave (one wave for all of them: 1.8 us against 0.8 for a
+    // share of the fours to each wave (one wave for all of them: 1.8 us against 1.1 for a
     // single token).
     const bool whole = first == 0 && last == tiles;
     constexpr int kFours = C::D / 8, kMine = kFours / C::KW;
@@ -750,8 +756,8 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
 
 // Query rows of a head, and the configurations that take them: up to 32 the waves have keys
 // of their own; more rows share them, 128 to a workgroup.  64 keys a step and two stages
-// against 32 keys and four (a barrier for every 16 KB): 213 us against 229 at 64 sequences x 17
-// nodes x 8192 keys, head 128; 155 against 171 at 2 x 64 nodes x 131001 keys, head 64.
+// against 32 keys and four (a barrier for every 16 KB): 203 us against 217 at 64 sequences x 17
+// nodes x 8192 keys, head 128; 147 against 162 at 2 x 64 nodes x 131001 keys, head 64.
 template <int D, class F>
 auto with_cfg(int64_t rows, F f) {
   if (rows <= 32) return f(Cfg<D, 4, 1, D == 64 ? 3 : 2, 1>{});

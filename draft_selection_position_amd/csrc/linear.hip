@@ -13,6 +13,12 @@
 // ring of stages; mfma_big.h's loads and waits), 16-byte chunk c of a row's eight at slot
 // c ^ ((row >> 1) & 7): the 16 rows that a fragment read touches then fall on distinct
 // banks.  Rows and k past the end of an operand read as zeros.
+//
+// What bounds it (MI355X): 4096 x 151936 x 5120, 2950 us, 2150 TFLOP/s: 64 KB a step into each
+// CU's LDS, which alone take 2240 us (18 bytes a clock, also where all of it hits the L2);
+// products and LDS reads without them take 1990.  Through registers instead they alone take
+// 1500, but the step as a whole is no faster for it (3050).  One row of 5120 x 4096, 6.6 us, and 16
+// of 151936 x 5120, 138 to 148: reading w.
 #include "dfs_device.h"
 #include "dfs_internal.h"
 #include "mfma_big.h"
@@ -602,16 +608,17 @@ hipError_t launch_stream(const LinearArgs& p, hipStream_t stream) {
 
 // Which kernel (times in us, bf16 output unless said, by rows x N x K):
 //   up to 16 rows  the streaming kernel from 16384 columns on, up to K = 5120 (16 x 151936 x 5120,
-//                  fp32: 148 against 182), else the one for few rows (1 x 5120 x 4096: 6.6)
-//   up to 32 rows  the same, the streaming one up to 24 blocks of k (its fragments of a spill beyond)
-//   up to 64 rows  128 x 64 tiles from 16384 columns on (64 x 60000 x 4096: 58 against 108), else the
-//                  kernel for few rows up to 48 (48 x 5120 x 4096: 11.8), then as for more
-//   more           256 x 256 tiles if there are four rounds of them (4096 x 151936 x 5120: 3055
-//                  against 4052 in 128 x 128), 128 x 128 from 300 on (1024 x 10240 x 5120: 89 against
-//                  111 in 64 x 64), else 64 x 64: one for each CU or less, and two groups of waves
+//                  fp32: 138 against 175), else the one for few rows (1 x 5120 x 4096: 6.6)
+//   up to 32 rows  the same, the streaming one up to 24 blocks of k (its fragments of a spill
+//                  beyond; 32 x 5120 x 4096: 9.9 against 11.3 in tiles)
+//   up to 64 rows  128 x 64 tiles from 16384 columns on (64 x 151936 x 5120: 153 against 177 in
+//                  64 x 64), else as for more
+//   more           256 x 256 tiles if there are four rounds of them (4096 x 151936 x 5120: 2950
+//                  against 3590 in 128 x 128), 128 x 128 from 300 on (1024 x 10240 x 5120: 82 against
+//                  108 in 64 x 64), else 64 x 64: one for each CU or less, and two groups of waves
 //                  take the blocks of k in turn (192 x 5120 x 5120: 13.5 against 17.5); two for each
 //                  or less, and one workgroup of eight waves takes two of them (333 x 5003 x 2064:
-//                  12.9 against 14.0; 512 x 5120 x 4096, 640 tiles: 26.6 against 23.9).  With an
+//                  12.9 against 14.1; 512 x 5120 x 4096, 640 tiles: 26.7 against 24.3).  With an
 //                  fp32 output (twice the matrix instructions) the latter gains nothing, and the
 //                  256 x 256 tile spills: 128 x 128 takes its place.
 template <bool kBf16>
@@ -624,7 +631,6 @@ hipError_t launch_linear(const LinearArgs& p, hipStream_t stream) {
     if (!columns) return launch_few<2, 2, 1, kBf16>(p, stream);
   }
   if (p.rows <= 64 && columns) return launch_tile<Wide, kBf16>(p, stream);
-  if (p.rows <= 48) return launch_few<3, 2, 1, kBf16>(p, stream);
   if constexpr (kBf16)
     if (cdiv(p.rows, Big::BR) * cdiv(p.N, Big::BN) >= 1024) return launch_tile<Big, kBf16>(p, stream);
   if (cdiv(p.rows, Mid::BR) * cdiv(p.N, Mid::BN) >= 300) return launch_tile<Mid, kBf16>(p, stream);

@@ -335,9 +335,8 @@ int dfs_lmhead_logits(const void* hidden, const void* W_lm, dfs_dtype_t dt, int6
  * scale for each group of 128 columns (the last group of a row may be shorter):
  *   s = x + residual;  y[c] = s[c] weight[c] / sqrt(mean(s^2) + eps)
  *   scale[g] = max(max_{c in g} |y[c]| / 448, 2^-100);  q[c] = e4m3(y[c] / scale[g])
- * all in fp32; s is not rounded before it is normalised, and y / scale is formed as
- * y (1 / scale), so a value within a few fp32 steps of the border between two e4m3 values
- * may go to either.  A row whose sum of squares is not finite in fp32 gives NaN throughout;
+ * s, its norm, y and the scales in fp32; s is not rounded before it is normalised, and
+ * y / scale = 448 s weight / max|s weight| is formed in 64 bits and rounded once.  A row whose sum of squares is not finite in fp32 gives NaN throughout;
  * a NaN or an infinity among a group's y gives it that scale, and NaN for what is not
  * finite / finite.
  *   x, residual (NULL: none), weight, out_total, out_norm of dtype dt
