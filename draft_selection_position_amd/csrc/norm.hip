@@ -11,9 +11,9 @@
 // what is normalised.
 //
 // The quotient.  1 / sqrt(...) is common to a group, so y / scale = 448 s w / max|s w|: taken in
-// 64 bits, where s w is exact, and rounded to e4m3 once (by way of 20 bits with a sticky last
-// one).  In fp32 its four or five roundings moved a few of a million values, those that lie
-// next to the border of two e4m3 steps, to the other step.
+// 64 bits, where s w is exact, and rounded to fp32 and from there to e4m3, as a quotient of 64
+// bits is converted.  In fp32 its four or five roundings moved a few of a million values, those
+// that lie next to the border of two e4m3 steps, to the other step.
 #include "dfs_device.h"
 #include "dfs_internal.h"
 
@@ -91,14 +91,6 @@ __device__ __forceinline__ double max_ror(double x) {
 }
 __device__ __forceinline__ double row16_max(double x) {
   return max_ror<0x121>(max_ror<0x122>(max_ror<0x124>(max_ror<0x128>(x))));
-}
-
-// To fp32 with the last of 20 bits odd where something was cut off: what is then rounded to
-// fewer bits is rounded as the double would have been.
-__device__ __forceinline__ float sticky20(double x) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, x);
-  const uint32_t hi = (uint32_t)(u >> 32) | ((uint32_t)u != 0 ? 1u : 0u);
-  return (float)__builtin_bit_cast(double, (uint64_t)hi << 32);
 }
 
 __device__ __forceinline__ float wave_sum(float v, int lane) {
@@ -181,7 +173,7 @@ __global__ __launch_bounds__(kWaves == 1 ? 4 * kWave : kWaves* kWave) void norm_
       k = scale > 0x1p-100f ? fma(fma(-pmost, k, 1.0), k, k) * (double)kE4m3Max : (double)inv * 0x1p100;
       if (top < INFINITY) {
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) y[j] = sticky20(p[j] * k);
+        for (int j = 0; j < kVec; ++j) y[j] = (float)(p[j] * k);
       } else {  // over an infinite scale: 0 or, where y is not finite itself, NaN
 #pragma unroll
         for (int j = 0; j < kVec; ++j) y[j] *= top != top ? NAN : 0.f;

@@ -336,9 +336,9 @@ int dfs_lmhead_logits(const void* hidden, const void* W_lm, dfs_dtype_t dt, int6
  *   s = x + residual;  y[c] = s[c] weight[c] / sqrt(mean(s^2) + eps)
  *   scale[g] = max(max_{c in g} |y[c]| / 448, 2^-100);  q[c] = e4m3(y[c] / scale[g])
  * s, its norm, y and the scales in fp32; s is not rounded before it is normalised, and
- * y / scale = 448 s weight / max|s weight| is formed in 64 bits and rounded once.  A row whose sum of squares is not finite in fp32 gives NaN throughout;
- * a NaN or an infinity among a group's y gives it that scale, and NaN for what is not
- * finite / finite.
+ * y / scale = 448 s weight / max|s weight| is formed in 64 bits and converted by way of
+ * fp32.  A row whose sum of squares is not finite in fp32 gives NaN throughout; a NaN or an
+ * infinity among a group's y gives it that scale, and NaN for what is not finite / finite.
  *   x, residual (NULL: none), weight, out_total, out_norm of dtype dt
  *   out_q [rows, d] e4m3;  out_scale [ceil(d / 128), rows] fp32 (a group's scales of all
  *   rows are adjacent, the order in which dfs_linear_q8 takes them)

@@ -94,16 +94,16 @@ def test_norm_many_rows(dfs, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_norm_values_are_rounded_once(dfs, dtype):
-    """Without a residual s is exact, and so is the quotient's side of every border between two steps: the
-    kernel forms it in 64 bits (an exact product, a reciprocal of two Newton steps: within 2^-45)."""
+def test_norm_quotients(dfs, dtype):
+    """Without a residual s is exact, and the kernel forms the quotient in 64 bits (an exact product, a reciprocal
+    of two Newton steps: within 2^-45): it is the 64-bit quotient rounded to fp32, whose conversion to e4m3 follows."""
     g = gen(8)
     for rows, d in ((1003, 4112), (4000, 1040)):
         x, w = randn(g, rows, d, dtype=dtype), (1 + 0.3 * randn(g, d)).to(dtype)
         v = tp.norm_q8(f64(x), f64(w), None, 1e-5)[2]
         q = f64(dfs.norm_q8(x, w, None, 1e-5, False)[0])
-        near = np.abs(v) * 2.0 ** -40
-        lo, hi = tp.e4m3_round(v - near), tp.e4m3_round(np.minimum(v + near, 463.0))
+        near = np.abs(v) * 2.0 ** -45
+        lo, hi = (tp.e4m3_round((v + e).astype(np.float32).astype(np.float64)) for e in (-near, near))
         assert ((q >= np.minimum(lo, hi)) & (q <= np.maximum(lo, hi))).all()
 
 
