@@ -177,7 +177,9 @@ struct Loader {
     const int row = 8 * (isw ? j : j - C::BN / 8);
     const int left = max((isw ? nn : nr) - row, 0);
     int pitch = K;
-    asm volatile("" : "+s"(pitch));  // formed anew every time: kept across steps, the resources of all loads spill
+    // formed anew every time where a wave has many: kept across steps, the resources of all
+    // loads spill (with four the asm costs 3 to 6%)
+    if constexpr (C::kLoads > 4) asm volatile("" : "+s"(pitch));
     const big::rsrc_t r = big::span_rsrc((isw ? w : a) + row * pitch, left * pitch);
     uint32_t voff = off + (uint32_t)ks * kBlock;
     if ((ks + 1) * kBlock > K && ks * kBlock + chunk >= K) voff = kPastEnd;
