@@ -333,6 +333,18 @@ def test_attention_ignores_what_is_not_seen(dfs, D, T, group):
         assert (got[kill] == 0).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,group,page", [(3, 2, 8), (16, 4, 64), (17, 4, 16), (64, 2, 128)])
+def test_attention_nodes_behind_the_last_keys(dfs, D, T, group, page):
+    """Every place that a sequence's last keys and its nodes can take in a tile; what lies behind a cache's last
+    position (NaN here) is not read into anything."""
+    lens = list(range(130)) + [191, 192, 193]
+    a = make(9, lens, T, 1, group, D, page, "holes", fill=float("nan"))
+    check_attention(dfs, *a)
+    one = dfs.tree_attention(*[t[70:71].contiguous() for t in a[:4]], a[4], a[5], a[6][70:71], a[7][70:71])
+    check_attention(dfs, *[t[70:71].contiguous() for t in a[:4]], a[4], a[5], a[6][70:71], a[7][70:71], got=one)
+
+
 def test_attention_infinite_values(dfs):
     """An infinite V of the last position and of a node: infinite where it is seen, the sign kept."""
     for T, group in ((3, 2), (40, 2)):
