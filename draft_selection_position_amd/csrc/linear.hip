@@ -615,9 +615,13 @@ hipError_t launch_stream(const LinearArgs& p, hipStream_t stream) {
 //                  beyond; 32 x 5120 x 4096: 9.9 against 11.3 in tiles)
 //   up to 64 rows  128 x 64 tiles from 16384 columns on (64 x 151936 x 5120: 153 against 177 in
 //                  64 x 64), else as for more
-//   more           256 x 256 tiles if there are four rounds of them (4096 x 151936 x 5120: 2950
-//                  against 3590 in 128 x 128), 128 x 128 from 300 on (1024 x 10240 x 5120: 82 against
-//                  108 in 64 x 64), else 64 x 64: one for each CU or less, and two groups of waves
+//   more           256 x 256 tiles, one to a CU, or 128 x 128 from 300 on, two to a CU (1024 x 10240 x
+//                  5120: 82 against 108 in 64 x 64), by their rounds: a round of the large ones
+//                  takes 1600 / 1024 of a round of the others, whose last, if short, takes half of
+//                  one and half of its share (4096 x 151936 x 5120: 2950 against 3590; 4096 x 4096 x
+//                  4096: 69 against 85; 1024 x 65536 x 2048: 156 against 199; 2048 x 5120 x 5120, 640
+//                  small ones: 77 against 78; 2560 x 8192 x 4096, 320 large ones: 121 against 109).
+//                  Fewer: 64 x 64: one for each CU or less, and two groups of waves
 //                  take the blocks of k in turn (192 x 5120 x 5120: 13.5 against 17.5); two for each
 //                  or less, and one workgroup of eight waves takes two of them (333 x 5003 x 2064:
 //                  12.9 against 14.1; 512 x 5120 x 4096, 640 tiles: 26.7 against 24.3).  With an
@@ -633,9 +637,11 @@ hipError_t launch_linear(const LinearArgs& p, hipStream_t stream) {
     if (!columns) return launch_few<2, 2, 1, kBf16>(p, stream);
   }
   if (p.rows <= 64 && columns) return launch_tile<Wide, kBf16>(p, stream);
+  const int64_t big = cdiv(p.rows, Big::BR) * cdiv(p.N, Big::BN), mid = cdiv(p.rows, Mid::BR) * cdiv(p.N, Mid::BN);
   if constexpr (kBf16)
-    if (cdiv(p.rows, Big::BR) * cdiv(p.N, Big::BN) >= 1024) return launch_tile<Big, kBf16>(p, stream);
-  if (cdiv(p.rows, Mid::BR) * cdiv(p.N, Mid::BN) >= 300) return launch_tile<Mid, kBf16>(p, stream);
+    if (1600 * cdiv(big, 256) < 1024 * (mid / 512) + (mid % 512 ? 512 + mid % 512 : 0))
+      return launch_tile<Big, kBf16>(p, stream);
+  if (mid >= 300) return launch_tile<Mid, kBf16>(p, stream);
   const int64_t tiles = cdiv(p.rows, Small::BR) * cdiv(p.N, Small::BN);
   if (tiles <= 256) return launch_tile<Pair, kBf16>(p, stream);
   if constexpr (kBf16)

@@ -194,6 +194,12 @@ def test_linear_middling_rows(dfs, rows, N, K):
     check_linear(dfs, gen(rows - K), rows, N, K, torch.float32)
 
 
+@pytest.mark.parametrize("rows,N,K", [(4096, 4096, 144), (2049, 7001, 400), (3001, 5003, 1040)])
+def test_linear_large_tiles(dfs, rows, N, K):
+    """One round of 256 x 256 tiles, whole and cut off at both ends."""
+    check_linear(dfs, gen(rows + K), rows, N, K, torch.bfloat16)
+
+
 def test_linear_values_that_are_not_finite(dfs):
     """A NaN or an infinite scale reaches its own row or column only (the matrix core reads whole tiles)."""
     g = gen(3)
