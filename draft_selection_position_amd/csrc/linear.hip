@@ -97,17 +97,21 @@ __device__ __forceinline__ uint32_t bf16_bits(float f) {
   return f != f ? 0x7fc0u : (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
 }
 
-// Four neighbouring columns n .. n + 3 of a row; `whole`: N is a multiple of 4.
+// Rows of an output start at any multiple of a value, so vectors go out unaligned (2394 x 139762 x 416,
+// bf16: 358 us, and 529 with single values wherever N was no multiple of 8).
+typedef uint2 __attribute__((aligned(2))) uint2_any;
+typedef uint4 __attribute__((aligned(2))) uint4_any;
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+
+// Four neighbouring columns n .. n + 3 of a row.
 template <bool kBf16>
-__device__ __forceinline__ void store4(void* out, int64_t row, int64_t N, int64_t n, f32x4 v, bool whole) {
-  if (whole) {
-    if (n < N) {
-      if constexpr (kBf16)
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + row * N + n) =
-            make_uint2(bf16_bits(v.x) | (bf16_bits(v.y) << 16), bf16_bits(v.z) | (bf16_bits(v.w) << 16));
-      else
-        *reinterpret_cast<f32x4*>(static_cast<float*>(out) + row * N + n) = v;
-    }
+__device__ __forceinline__ void store4(void* out, int64_t row, int64_t N, int64_t n, f32x4 v) {
+  if (n + 4 <= N) {
+    if constexpr (kBf16)
+      *reinterpret_cast<uint2_any*>(static_cast<uint16_t*>(out) + row * N + n) =
+          make_uint2(bf16_bits(v.x) | (bf16_bits(v.y) << 16), bf16_bits(v.z) | (bf16_bits(v.w) << 16));
+    else
+      *reinterpret_cast<f32x4_any*>(static_cast<float*>(out) + row * N + n) = v;
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -343,7 +347,6 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void linear_q8_tile_kern
   static_assert(C::kWaves * 16 * kPitch * (int)sizeof(Out) <= C::kLds, "the tiles' LDS");
   Out* mine = reinterpret_cast<Out*>(lds) + wave * 16 * kPitch;
   const int col0 = n0 + kCols * wn, cols = min(kCols, (int)p.N - col0);
-  const bool whole = (p.N * sizeof(Out)) % 16 == 0;
 #pragma unroll
   for (int j = 0; j < C::TR; ++j) {
 #pragma unroll
@@ -358,19 +361,17 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void linear_q8_tile_kern
     }
     const int row0 = r0 + 16 * (C::TR * wr + j), rows = min(16, (int)p.rows - row0);
     Out* out = static_cast<Out*>(p.out) + (int64_t)row0 * p.N + col0;
-    if (whole) {
-      constexpr int kVec = 16 / sizeof(Out), kPer = kCols / kVec;
+    constexpr int kVec = 16 / sizeof(Out), kPer = kCols / kVec;
 #pragma unroll
-      for (int u = lane; u < 16 * kPer; u += 64) {
-        const int y = u / kPer, x = u % kPer * kVec;
-        if (y < rows && x < cols)
-          *reinterpret_cast<uint4*>(out + y * p.N + x) = *reinterpret_cast<const uint4*>(mine + y * kPitch + x);
-      }
-    } else {
-      for (int u = lane; u < 16 * kCols; u += 64) {
-        const int y = u / kCols, x = u % kCols;
-        if (y < rows && x < cols) out[y * p.N + x] = mine[y * kPitch + x];
-      }
+    for (int u = lane; u < 16 * kPer; u += 64) {
+      const int y = u / kPer, x = u % kPer * kVec;
+      if (y < rows && x + kVec <= cols)
+        *reinterpret_cast<uint4_any*>(out + y * p.N + x) = *reinterpret_cast<const uint4*>(mine + y * kPitch + x);
+    }
+    if (cols % kVec != 0 && cols < kCols) {  // the last columns, behind the last whole vector
+      const int y = lane >> 2;
+      for (int x = max(cols, 0) / kVec * kVec + (lane & 3); x < cols; x += 4)
+        if (y < rows) out[y * p.N + x] = mine[y * kPitch + x];
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before it is written again
   }
@@ -468,13 +469,12 @@ __global__ __launch_bounds__(512) void linear_q8_few_kernel(LinearArgs p) {
 #pragma unroll
     for (int j = 0; j < RT; ++j) part[wave][i * RT + j][lane] = acc[i][j];
   __syncthreads();
-  const bool whole = (p.N & 3) == 0;
   for (int t = wave; t < MT * RT; t += W) {
     f32x4 v = part[0][t][lane];
 #pragma unroll
     for (int w = 1; w < W; ++w) v += part[w][t][lane];
     const int i = t / RT, j = t % RT;
-    if (16 * j + r < p.rows) store4<kBf16>(p.out, 16 * j + r, p.N, n0 + 16 * i + 4 * g, v, whole);
+    if (16 * j + r < p.rows) store4<kBf16>(p.out, 16 * j + r, p.N, n0 + 16 * i + 4 * g, v);
   }
 }
 
@@ -549,7 +549,6 @@ __global__ __launch_bounds__(512, 2) void linear_q8_stream_kernel(LinearArgs p) 
     for (int j = 0; j < RT; ++j) to[wave][j][lane] = acc[j];
     __builtin_amdgcn_sched_barrier(0);
   };
-  const bool whole = (p.N & 3) == 0;
   // The sums of four tiles (or the n last ones): a wave takes four rows, 16 lanes a row's 64 columns.
   auto reduce = [&](f32x4 (&from)[GT][W][RT][64], int i, int n) {
     big::bar();
@@ -560,7 +559,7 @@ __global__ __launch_bounds__(512, 2) void linear_q8_stream_kernel(LinearArgs p) 
 #pragma unroll
       for (int w = 1; w < W; ++w) v += from[u][w][j][src];
       if (16 * j + row < p.rows)
-        store4<kBf16>(p.out, 16 * j + row, p.N, (int64_t)tile_at(i + u) * 16 + 4 * (lane & 3), v, whole);
+        store4<kBf16>(p.out, 16 * j + row, p.N, (int64_t)tile_at(i + u) * 16 + 4 * (lane & 3), v);
     }
   };
   load(c[0], 0);
