@@ -54,8 +54,9 @@ struct AttnArgs {
   uint16_t* out;
   float* part_o;   // [Hkv, row tiles, 2 G, rows of a tile, D]
   float* part_ml;  // [Hkv, row tiles, 2 G, rows of a tile, 2]: maximum and sum; of an unused node's row the last piece has kUnused
-  int2* pieces;    // [batch]: the first and the last part with a tile of the sequence
+  int2* pieces;    // [batch]: the first and the last part with a tile of the sequence (NULL: nothing to join)
   int batch, T, group, G, row_tiles;
+  bool whole;  // parts are sequences
   int spread;  // 16-lane groups that join a row's pieces: 1, 4 or 16
   float c2;  // scale * log2(e)
 };
@@ -142,6 +143,12 @@ __device__ __forceinline__ uint64_t shfl64(uint64_t x, int src) {
 template <class C>
 __device__ __forceinline__ int seq_tiles(const AttnArgs& a, int b) {
   return (a.c.len(b) + a.T + C::kTile - 1) / C::kTile;
+}
+
+// Parts that `total` tiles are cut into: from 32 a sequence on of four tiles or more, as the join reads every
+// row once for each (84 rows, 2 x 23520 keys: 23.3 us against 32.3; 68 rows, 4001: 20.4 against 23.0).
+__device__ __forceinline__ int parts_of(const AttnArgs& a, int total) {
+  return min(min(a.G, total), max(32 * a.batch, (total + 3) / 4));
 }
 
 // a b / c rounded down, for a b < 2^53 and c < 2^32: the quotient is at least 1 / c away from
@@ -373,20 +380,26 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
   const int unit = turn * 8 + blockIdx.x % 8;  // (head, part)
   if (unit >= Hkv * a.G) return;
   const int head = unit / a.G, g = unit % a.G;
-  // part g of min(G, total): the tiles x .. x_end - 1, at least one
-  const Where w = locate<C>(a, scratch, [&](int total) {
-    return min(mul_div(g, total, min(a.G, total)), total - 1);
-  });
-  const int total = uniform(w.total), parts = min(a.G, total);
-  if (g >= parts) return;
-  int x = uniform(mul_div(g, total, parts));
-  const int x_end = uniform(mul_div(g + 1, total, parts)), steps = x_end - x;
+  // part g: the tiles x .. x_end - 1, at least one
+  int x = 0, x_end, seq = g, before = 0, total = 0, parts = 0;
+  if (a.whole) {
+    x_end = seq_tiles<C>(a, g);
+  } else {
+    const Where w = locate<C>(a, scratch, [&](int total) {
+      return min(mul_div(g, total, parts_of(a, total)), total - 1);
+    });
+    total = uniform(w.total), parts = parts_of(a, total);
+    if (g >= parts) return;
+    x = uniform(mul_div(g, total, parts));
+    x_end = uniform(mul_div(g + 1, total, parts));
+    seq = uniform(w.seq), before = uniform(w.before);
+  }
+  const int steps = x_end - x;
   if constexpr (C::kEven) __builtin_amdgcn_s_setprio(3);
   const int rows = a.T * a.group;
   const int row = rt * C::kRows + 32 * rw + (lane & 31);
   const int qrow = min(row, rows - 1), t = qrow / a.group, gh = qrow % a.group;
   const int h = lane >> 5;
-  int seq = uniform(w.seq), before = uniform(w.before);
   const int64_t slot0 = ((int64_t)head * a.row_tiles + rt) * 2 * a.G;
   const Frag<C> at(lane);
   const uint32_t ring0 = lds_addr(lds) + kw * C::S * C::kStage;
@@ -400,7 +413,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
     const int tiles = (len + a.T + C::kTile - 1) / C::kTile;
     const int first = x - before, last = min(tiles, x_end - before);
     // for the join: tile y is in part floor(((y + 1) parts - 1) / total)
-    if (a.G > 1 && first == 0 && head == 0 && rt == 0 && threadIdx.x == 0)
+    if (a.pieces && first == 0 && head == 0 && rt == 0 && threadIdx.x == 0)
       a.pieces[seq] = make_int2(g, (int)(((double)(before + tiles) * (double)parts - 1.0) / (double)total));
     const int n = last - first;  // steps
     const int32_t* table = a.c.block_table + (int64_t)seq * a.c.table_width;
@@ -748,7 +761,7 @@ template <class C>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
   tree_attention_kernel<C><<<dim3((uint32_t)(cdiv((int64_t)a.G * a.c.kv_heads, 8) * 8 * a.row_tiles)), dim3(C::kThreads), 0, stream>>>(a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.G == 1) return e;
+  if (e != hipSuccess || !a.pieces) return e;
   tree_attention_join_kernel<C><<<
       dim3((uint32_t)(a.batch * a.c.kv_heads * cdiv(a.T * a.group, 16 / a.spread))), dim3(256), 0, stream>>>(a);
   return hipGetLastError();
@@ -775,14 +788,19 @@ AttnPlan plan_tree_attention(const CacheView& c, int64_t batch, int64_t T, int64
     AttnPlan p{};
     p.row_tiles = cdiv(rows, C::kRows);
     // tiles when all lengths are full: no more parts than that
-    const int64_t most =
-        batch * cdiv(((int64_t)c.table_width << c.page_shift) + T, (int64_t)C::kTile);
+    const int64_t each = cdiv(((int64_t)c.table_width << c.page_shift) + T, (int64_t)C::kTile), most = batch * each;
     p.G = 256 * C::kGroups / (p.row_tiles * c.kv_heads);
     p.G = p.G < 1 ? 1 : p.G > most ? most : p.G;
+    // Few tiles a sequence at most: a part for each and no join (4 x 9 nodes, page 256: 8.0 us
+    // against 10.2; 39 x 33 nodes, up to 61 keys: 17.8 against 24.4; 13 x 56 nodes, 7 heads, 243 keys: 16.2
+    // against 27.9; at worst 2 x 18 nodes, 3 heads, 115 keys: 14.0 against 12.8).
+    p.whole = each <= 4 || (each <= 8 && batch * c.kv_heads * p.row_tiles >= 48);
+    if (p.whole) p.G = batch;
     const int64_t slots = (int64_t)c.kv_heads * p.row_tiles * 2 * p.G * C::kRows;
-    p.part_bytes = p.G > 1 ? align_up((size_t)(slots * D) * 4, 256) : 0;
-    p.ml_bytes = p.G > 1 ? align_up((size_t)slots * 8, 256) : 0;
-    p.ws_bytes = p.G > 1 ? p.part_bytes + p.ml_bytes + align_up((size_t)batch * 8, 256) : 0;
+    const bool join = p.G > 1 && !p.whole;
+    p.part_bytes = join ? align_up((size_t)(slots * D) * 4, 256) : 0;
+    p.ml_bytes = join ? align_up((size_t)slots * 8, 256) : 0;
+    p.ws_bytes = join ? p.part_bytes + p.ml_bytes + align_up((size_t)batch * 8, 256) : 0;
     return p;
   };
   return D == 64 ? with_cfg<64>(rows, plan) : with_cfg<128>(rows, plan);
@@ -800,7 +818,8 @@ hipError_t launch_tree_attention(const AttnPlan& p, const CacheView& c, const vo
   a.out = static_cast<uint16_t*>(out);
   a.part_o = static_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_bytes);
-  a.pieces = reinterpret_cast<int2*>(static_cast<char*>(ws) + p.part_bytes + p.ml_bytes);
+  a.pieces = p.ws_bytes == 0 ? nullptr : reinterpret_cast<int2*>(static_cast<char*>(ws) + p.part_bytes + p.ml_bytes);
+  a.whole = p.whole;
   a.batch = (int)batch;
   a.T = (int)T;
   a.group = (int)group;

@@ -225,6 +225,7 @@ hipError_t launch_cache_commit(const CacheView& c, const void* k_new, const void
 struct AttnPlan {
   int64_t row_tiles;       // workgroups for a head's rows
   int64_t G;               // parts that the keys of a head are cut into
+  bool whole;              // parts are sequences: nothing to join
   size_t part_bytes;       // of the parts' fp32 sums,
   size_t ml_bytes;         // of their maxima and sums; each sequence's parts follow
   size_t ws_bytes;

@@ -266,7 +266,7 @@ def test_binding_refuses(dfs):
         with pytest.raises((ValueError, TypeError)):
             dfs.tree_attention(*at[:i], bad, *at[i + 1:])
     with pytest.raises(ValueError):
-        dfs.tree_attention(*at, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        dfs.tree_attention(*make(92, [2000, 3], 3, 2, 2, 64, 16), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(dfs.DfsError):
         dfs.tree_attention(*at, scale=0.0)
     with pytest.raises(dfs.DfsError):

@@ -165,9 +165,12 @@ def test_tree_attention_refusals(L):
         assert f(scale=scale) == E_ARG
     for i in range(len(names)):
         assert f(out=P + (i << 36)) == E_ARG
-    need = L.dfs_tree_attention_workspace_bytes(ctypes.byref(_shape()))
-    assert need > 0 and f(ws=None) == E_WS and f(wsb=need - 1) == E_WS and f(ws=FAR + (1 << 40) + 8) == E_ALIGN
-    assert passes(f)
+    assert L.dfs_tree_attention_workspace_bytes(ctypes.byref(_shape())) == 0  # few cached keys at most: nothing is cut
+    long = dict(table_width=400)
+    need = L.dfs_tree_attention_workspace_bytes(ctypes.byref(_shape(**long)))
+    assert need > 0 and f(long, ws=None) == E_WS and f(long, wsb=need - 1) == E_WS
+    assert f(ws=FAR + (1 << 40) + 8) == E_ALIGN and f(long, ws=FAR + (1 << 40) + 8) == E_ALIGN
+    assert passes(f) and passes(f, shape=long)
 
 
 def test_cache_commit_refusals(L):
