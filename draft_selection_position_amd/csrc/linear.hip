@@ -620,12 +620,13 @@ hipError_t launch_stream(const LinearArgs& p, hipStream_t stream) {
 //                  one and half of its share (4096 x 151936 x 5120: 2950 against 3590; 4096 x 4096 x
 //                  4096: 69 against 85; 1024 x 65536 x 2048: 156 against 199; 2048 x 5120 x 5120, 640
 //                  small ones: 77 against 78; 2560 x 8192 x 4096, 320 large ones: 121 against 109).
-//                  Fewer: 64 x 64: one for each CU or less, and two groups of waves
-//                  take the blocks of k in turn (192 x 5120 x 5120: 13.5 against 17.5); two for each
-//                  or less, and one workgroup of eight waves takes two of them (333 x 5003 x 2064:
-//                  12.9 against 14.1; 512 x 5120 x 4096, 640 tiles: 26.7 against 24.3).  With an
-//                  fp32 output (twice the matrix instructions) the latter gains nothing, and the
-//                  256 x 256 tile spills: 128 x 128 takes its place.
+//                  Fewer: 64 x 64.  One for each CU or less, and two groups of waves take the blocks
+//                  of k in turn (192 x 5120 x 5120: 13.3 against 16.6).  Two for each or less, and
+//                  more than three, and one workgroup of eight waves takes two of them (333 x 5003 x
+//                  2064: 11.7 against 12.8; 640 x 6000 x 4096, 940 tiles: 27.9 against 32.3; but 512 x 5120
+//                  x 4096, 640 tiles: 26.4 against 23.3).  With an fp32 output (twice the matrix
+//                  instructions) that is so beyond three only (333 x 5003 x 2064: 17.3 against 16.4),
+//                  and the 256 x 256 tile spills: 128 x 128 takes its place.
 template <bool kBf16>
 hipError_t launch_linear(const LinearArgs& p, hipStream_t stream) {
   const bool columns = p.N >= 16384;
@@ -643,8 +644,7 @@ hipError_t launch_linear(const LinearArgs& p, hipStream_t stream) {
   if (mid >= 300) return launch_tile<Mid, kBf16>(p, stream);
   const int64_t tiles = cdiv(p.rows, Small::BR) * cdiv(p.N, Small::BN);
   if (tiles <= 256) return launch_tile<Pair, kBf16>(p, stream);
-  if constexpr (kBf16)
-    if (tiles <= 512) return launch_tile<Tall, kBf16>(p, stream);
+  if ((kBf16 && tiles <= 512) || tiles > 768) return launch_tile<Tall, kBf16>(p, stream);
   return launch_tile<Small, kBf16>(p, stream);
 }
 

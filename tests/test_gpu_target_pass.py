@@ -187,9 +187,10 @@ def test_linear_many_rows(dfs, rows, N, K):
     check_linear(dfs, gen(N + 1), rows, N, K, torch.float32)
 
 
-@pytest.mark.parametrize("rows,N,K", [(333, 5003, 2064), (700, 2001, 144), (1030, 1900, 1296), (65, 16300, 16)])
+@pytest.mark.parametrize("rows,N,K", [(333, 5003, 2064), (700, 2001, 144), (1030, 1900, 1296), (65, 16300, 16),
+                                     (640, 4000, 272), (768, 5003, 272)])
 def test_linear_middling_rows(dfs, rows, N, K):
-    """More 64 x 64 tiles than CUs, up to twice as many: workgroups of eight waves."""
+    """More 64 x 64 tiles than CUs, up to four times as many: workgroups of eight waves, or of four."""
     check_linear(dfs, gen(rows + K), rows, N, K, torch.bfloat16)
     check_linear(dfs, gen(rows - K), rows, N, K, torch.float32)
 
