@@ -61,13 +61,14 @@ struct AttnArgs {
   float c2;  // scale * log2(e)
 };
 
-// KW key groups x RW row groups of waves, a ring of S stages of 32 SUB keys.
-template <int D_, int KW_, int RW_, int S_, int SUB_ = 1>
+// KW key groups x RW row groups of waves, a ring of S stages of 32 SUB keys; kOnce: one workgroup
+// has all rows of a head.
+template <int D_, int KW_, int RW_, int S_, int SUB_ = 1, bool kOnce_ = true>
 struct Cfg {
   static constexpr int D = D_, KW = KW_, RW = RW_, S = S_;
   static_assert(KW == 1 || RW == 1, "waves share a tile, or have their own");
   static constexpr int kWaves = KW * RW, kThreads = 64 * kWaves;
-  static constexpr bool kOnce = RW < 4;  // one workgroup has all rows of a head
+  static constexpr bool kOnce = kOnce_;
   static constexpr int kRows = 32 * RW;            // query rows of a workgroup
   static constexpr int SUB = SUB_, kKeys = 32 * SUB;  // keys of a group's step
   static constexpr int kTile = KW * kKeys;         // of a workgroup's
@@ -146,7 +147,8 @@ __device__ __forceinline__ int seq_tiles(const AttnArgs& a, int b) {
 }
 
 // Parts that `total` tiles are cut into: from 32 a sequence on of four tiles or more, as the join reads every
-// row once for each (84 rows, 2 x 23520 keys: 23.3 us against 32.3; 68 rows, 4001: 20.4 against 23.0).
+// row once for each (68 rows of 128, 4001 keys: 20.4 us against 23.0; 84 of 64, 2 x 23520: 24.9, and 32
+// without this by three waves a workgroup).
 __device__ __forceinline__ int parts_of(const AttnArgs& a, int total) {
   return min(min(a.G, total), max(32 * a.batch, (total + 3) / 4));
 }
@@ -770,13 +772,17 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
 // Query rows of a head, and the configurations that take them: up to 32 the waves have keys
 // of their own; more rows share them, 128 to a workgroup.  64 keys a step and two stages
 // against 32 keys and four (a barrier for every 16 KB): 203 us against 217 at 64 sequences x 17
-// nodes x 8192 keys, head 128; 147 against 162 at 2 x 64 nodes x 131001 keys, head 64.
+// nodes x 8192 keys, head 128; 147 against 162 at 2 x 64 nodes x 131001 keys, head 64.  65 to 96 rows of
+// 128: three waves (211 us against 214 by four at 64 x 17 nodes x 8192 keys); of 64: four, an idle one
+// among them (122 against 145: by three, twelve waves on a CU, the registers do not suffice).
 template <int D, class F>
 auto with_cfg(int64_t rows, F f) {
   if (rows <= 32) return f(Cfg<D, 4, 1, D == 64 ? 3 : 2, 1>{});
   if (rows <= 64) return f(Cfg<D, 1, 2, 2, 2>{});
-  if (rows <= 96) return f(Cfg<D, 1, 3, 2, 2>{});
-  return f(Cfg<D, 1, 4, 2, 2>{});
+  if constexpr (D == 128)
+    if (rows <= 96) return f(Cfg<D, 1, 3, 2, 2>{});
+  if (rows <= 128) return f(Cfg<D, 1, 4, 2, 2>{});
+  return f(Cfg<D, 1, 4, 2, 2, false>{});
 }
 
 }  // namespace
