@@ -433,7 +433,8 @@ __global__ __launch_bounds__(512) void linear_q8_few_kernel(LinearArgs p) {
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       // k past K reads a row's own last 16 bytes; a's are then cleared, so that they count for
-      // nothing (what is not finite in a row of w makes its column so anyway)
+      // nothing (what is not finite in a row of w makes its column so anyway).  A block past the last
+      // is all such k, and takes a scale of zero: the last block's may be infinite.
       const int kb = min(kb0 + W * b, p.G - 1), k = (kb0 + W * b) * kBlock + 32 * g;
 #pragma unroll
       for (int i = 0; i < MT; ++i) fw[b][i] = load_frag(wrow[i], k, p.K);
@@ -460,7 +461,8 @@ __global__ __launch_bounds__(512) void linear_q8_few_kernel(LinearArgs p) {
       for (int i = 0; i < MT; ++i) {
         const Operand<true> ow(fw[b][i]);
 #pragma unroll
-        for (int j = 0; j < RT; ++j) add_scaled(acc[i][j], block_mfma(ow, oa[j]), sc[b][j] * wsc[b]);
+        for (int j = 0; j < RT; ++j)
+          add_scaled(acc[i][j], block_mfma(ow, oa[j]), b == 0 || kb0 + W * b < p.G ? sc[b][j] * wsc[b] : 0.f);
       }
     }
   }
@@ -516,6 +518,7 @@ __global__ __launch_bounds__(512, 2) void linear_q8_stream_kernel(LinearArgs p) 
       const int64_t row = min((int64_t)(16 * j + r), p.rows - 1);
       fa[b][j] = load_frag(p.a + row * p.K, k, p.K);
       sa[b][j] = p.a_scale[(int64_t)min(kb, p.G - 1) * p.rows + row];
+      if (kb >= p.G) sa[b][j] = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (k + 16 * (e / 4) >= p.K) fa[b][j][e] = 0;  // k past K counts for nothing (see above)
@@ -540,7 +543,8 @@ __global__ __launch_bounds__(512, 2) void linear_q8_stream_kernel(LinearArgs p) 
     for (int j = 0; j < RT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const float ws = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(c.scale), b));
+      float ws = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(c.scale), b));
+      if (b == NB - 1 && wave + W * b >= p.G) ws = 0.f;  // only the last one may lie past the last block
       const Operand<true> fw(c.w[b]);
 #pragma unroll
       for (int j = 0; j < RT; ++j) add_scaled(acc[j], block_mfma(fw, Operand<true>(fa[b][j])), sa[b][j] * ws);

@@ -1,0 +1,82 @@
+"""Every form that the 8-bit product's rule chooses, on the GPU against its definition in 64 bits.
+
+The rule goes by rows, columns and blocks of k, so each list below names the kernel that its sizes reach:
+few rows (one or two tiles of 16), the streaming kernel by its tiles and blocks a wave, and the tiles.
+Tolerances are the product's (see test_gpu_target_pass); tests on one value a row and block are exact.
+"""
+import pytest
+import torch
+
+from .test_gpu_target_pass import dfs, gen  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+FEW = [(1, 1000, 272), (16, 5003, 2064), (16, 17001, 5264), (17, 1000, 272), (32, 5003, 1040)]
+STREAM = [(5, 16385, 144), (16, 17001, 1040), (16, 17001, 2064), (16, 16389, 3088), (13, 17001, 4112), (16, 20003, 5120),
+          (17, 20003, 272), (32, 16391, 1040), (32, 20003, 2064), (29, 17001, 3056)]
+WIDE = [(33, 16387, 400), (64, 20003, 2064), (20, 16400, 3200), (48, 16390, 16)]
+PAIR = [(33, 130, 272), (150, 300, 1296)]
+TALL = [(333, 5003, 272), (640, 6000, 400)]          # bf16; the second one for fp32 too
+SMALL = [(512, 5125, 400), (333, 5003, 272)]         # bf16 and fp32; fp32
+MID = [(1000, 5003, 272), (1030, 10001, 144)]
+BIG = [(4096, 4096, 144), (2049, 7001, 400)]         # bf16; fp32 takes 128 x 128 tiles
+ALL = FEW + STREAM + WIDE + PAIR + TALL + SMALL[:1] + MID + BIG
+DTYPES = [torch.bfloat16, torch.float32]
+
+
+def in_64_bits(a, sa, w, sw):
+    """(out, the same over magnitudes), a block of k after the other."""
+    rows, N = a.shape[0], w.shape[0]
+    out = torch.zeros(rows, N, dtype=torch.float64, device=a.device)
+    mag = torch.zeros_like(out)
+    for g in range(sa.shape[0]):
+        x, y = a[:, 128 * g:128 * (g + 1)].double(), w[:, 128 * g:128 * (g + 1)].double()
+        f = sa[g].double()[:, None] * sw[:, g].double().repeat_interleave(128)[:N]
+        out += (x @ y.t()) * f
+        mag += (x.abs() @ y.abs().t()) * f.abs()
+    return out, mag
+
+
+def one_value_a_row(g, rows, N, K):
+    """Row r of a has one value, 1, at a k of its own, so that out is w's code there times two powers of two: exact,
+    in fp32 and in bf16.  w holds every code but the two NaN."""
+    at = torch.randperm(max(rows, K), generator=g, device="cuda")[:rows] % K
+    at[-1] = K - 1
+    a = torch.zeros(rows, K, device="cuda")
+    a[torch.arange(rows, device="cuda"), at] = 1.0
+    codes = torch.randint(0, 256, (N, K), generator=g, device="cuda").to(torch.uint8)
+    codes = torch.where(codes & 0x7F == 0x7F, codes & 0x80, codes)  # zeros of both signs in their place
+    G = -(-K // 128)
+    sa = 2.0 ** torch.randint(-6, 7, (G, rows), generator=g, device="cuda").float()
+    sw = 2.0 ** torch.randint(-6, 7, (-(-N // 128), G), generator=g, device="cuda").float()
+    return a.to(torch.float8_e4m3fn), sa, codes.view(torch.float8_e4m3fn), sw, at
+
+
+def same(got, want):
+    """Equal, NaN for NaN."""
+    return bool(((got == want) | (torch.isnan(got) & torch.isnan(want))).all())
+
+
+@pytest.mark.parametrize("rows,N,K", ALL)
+def test_infinite_scales(dfs, rows, N, K):
+    """An infinite scale of the last block of k, or of a block of columns there: infinite, with the product's sign,
+    where the definition is, and NaN only where it is (zero times infinity)."""
+    a, sa, w, sw, at = one_value_a_row(gen(rows + K), rows, N, K)
+    G = sa.shape[0]
+    for side in ("a", "w"):
+        sa2, sw2 = sa.clone(), sw.clone()
+        if side == "a":
+            sa2[G - 1, rows - 1] = float("inf")  # of the row whose value is in that block
+        else:
+            sw2[-1, G - 1] = float("inf")
+        want = in_64_bits(a, sa2, w, sw2)[0]
+        for dtype in DTYPES:
+            got = dfs.linear_q8(a, sa2, w, sw2, out_dtype=dtype).double()
+            assert same(got, want), (side, dtype, int(torch.isnan(got).sum()), int(torch.isnan(want).sum()))
