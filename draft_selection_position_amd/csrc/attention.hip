@@ -832,7 +832,7 @@ hipError_t launch_tree_attention(const AttnPlan& p, const CacheView& c, const vo
   a.G = (int)p.G;
   a.row_tiles = (int)p.row_tiles;
   a.spread = p.G >= 32 * batch ? 16 : p.G >= 8 * batch ? 4 : 1;  // by its pieces
-  a.c2 = (float)(scale * 1.4426950408889634);
+  a.c2 = attention_c2(scale);
   auto run = [&](auto cfg) { return launch<decltype(cfg)>(a, stream); };
   return D == 64 ? with_cfg<64>(T * group, run) : with_cfg<128>(T * group, run);
 }

@@ -690,7 +690,9 @@ int dfs_tree_attention(const void* q, const void* k_new, const void* v_new, cons
       !aligned(v_pages, 16) || !aligned(out, 16) || !aligned(parents, 4) || !aligned(block_table, 4) ||
       !aligned(lens, 4))
     return DFS_E_ALIGN;
-  if (!(std::isfinite(scale) && scale > 0.0)) return DFS_E_ARG;
+  // as the kernel takes it: a factor of zero or infinity would make NaN of masked scores, or of zeros
+  const float c2 = attention_c2(scale);
+  if (!(std::isfinite(c2) && c2 > 0.f)) return DFS_E_ARG;
   const size_t qn = (size_t)(s.batch * s.T * s.q_heads * s.head_dim) * 2, nn = nodes_bytes(s), pn = pool_bytes(s);
   if (overlaps(out, qn, q, qn) || overlaps(out, qn, k_new, nn) || overlaps(out, qn, v_new, nn) ||
       overlaps(out, qn, k_pages, pn) || overlaps(out, qn, v_pages, pn) ||

@@ -230,6 +230,8 @@ struct AttnPlan {
   size_t ml_bytes;         // of their maxima and sums; each sequence's parts follow
   size_t ws_bytes;
 };
+// Scores' factor in the kernel's exponent: powers of two.
+inline float attention_c2(double scale) { return (float)(scale * 1.4426950408889634); }
 AttnPlan plan_tree_attention(const CacheView& c, int64_t batch, int64_t T, int64_t group, int64_t D);
 hipError_t launch_tree_attention(const AttnPlan& p, const CacheView& c, const void* q, const void* k_new,
                                  const void* v_new, const int32_t* parents, int64_t batch, int64_t T, int64_t group,

@@ -401,7 +401,8 @@ typedef struct {
  *   int32: entries past a sequence's length are not read, and those that are, clamped to the pool.
  * What is not finite in a key or value that a row does not see does not reach the row.
  * Scores, maxima, sums and the accumulated output in fp32; softmax weights are rounded to
- * bf16 for the matrix cores.  dtype must be DFS_BF16; scale finite and > 0.  The order of
+ * bf16 for the matrix cores.  dtype must be DFS_BF16; scale > 0, and scale * log2(e) neither
+ * zero nor infinite in fp32 (1e-45 to 2.3e38).  The order of
  * sums depends on all lengths of the batch: the same call gives the same bits, the same
  * sequence in another batch need not.  Alignment: the int32 arrays 4 bytes, everything else 16,
  * ws 256.  out overlaps no input.

@@ -1,0 +1,18 @@
+"""Arguments of the verification pass's operators at the ends of their ranges (CPU)."""
+import ctypes
+
+from .test_target_pass_oracle import E_ARG, FAR, L, P, _shape, passes  # noqa: F401
+
+FP32_MAX, FP32_TINY = 3.4028234663852886e38, 2.0 ** -149
+
+
+def test_a_scale_outside_fp32_is_refused(L):  # noqa: F811
+    """The kernel multiplies scores by fp32(scale * log2(e)): neither zero nor infinite."""
+    def f(scale):
+        a = [P + (i << 36) for i in range(8)]
+        return L.dfs_tree_attention(*a, ctypes.byref(_shape()), scale, FAR, FAR + (1 << 40), 1 << 36, None)
+
+    for scale in (1e-300, 1e-46, FP32_TINY / 4, FP32_MAX, 2.4e38, 1e300):
+        assert f(scale) == E_ARG, scale
+    for scale in (FP32_TINY, 1e-30, 1.0, 2.3e38):
+        assert passes(f, scale), scale
