@@ -575,7 +575,10 @@ int dfs_norm_q8(const void* x, const void* residual, const void* weight, dfs_dty
   if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(out_q, 16) ||
       !aligned(out_scale, 4) || !aligned(out_total, 16) || !aligned(out_norm, 16))
     return DFS_E_ALIGN;
-  if (!(std::isfinite(eps) && eps >= 0.0) || (out_total && !residual)) return DFS_E_ARG;
+  // as the kernel takes it: a positive eps that becomes zero makes a row of zeros NaN
+  const float eps32 = (float)eps;
+  if (!(std::isfinite(eps32) && eps >= 0.0) || (eps > 0.0 && eps32 == 0.f)) return DFS_E_ARG;
+  if (out_total && !residual) return DFS_E_ARG;
   const size_t n = (size_t)(rows * d) * esize(dt), wn = (size_t)d * esize(dt);
   const size_t qn = (size_t)(rows * d), sn = (size_t)(rows * cdiv(d, 128)) * 4;
   struct Span {
@@ -596,7 +599,7 @@ int dfs_norm_q8(const void* x, const void* residual, const void* weight, dfs_dty
   int st = check_device();
   if (st != DFS_OK) return st;
   (void)hipGetLastError();
-  return hip_status(launch_norm_q8(x, residual, weight, dt == DFS_BF16, rows, d, (float)eps, out_q, out_scale,
+  return hip_status(launch_norm_q8(x, residual, weight, dt == DFS_BF16, rows, d, eps32, out_q, out_scale,
                                    out_total, out_norm, stream));
 }
 

@@ -345,8 +345,9 @@ int dfs_lmhead_logits(const void* hidden, const void* W_lm, dfs_dtype_t dt, int6
  *   out_total [rows, d] = s rounded (NULL: not wanted; needs a residual); it may be x or
  *   residual itself, and otherwise overlaps neither;  out_norm [rows, d] = y rounded (NULL:
  *   not wanted)
- * d a multiple of 16 in [16, 65536], 1 <= rows <= DFS_MAX_ROWS, rows * d <= 2^35; eps finite and
- * >= 0 (0 with a row of zeros: NaN).  Alignment: out_scale 4 bytes, everything else 16.     */
+ * d a multiple of 16 in [16, 65536], 1 <= rows <= DFS_MAX_ROWS, rows * d <= 2^35; eps 0 (a row
+ * whose squares are zeros in fp32 is then not finite), or positive and neither zero nor infinite in
+ * fp32.  Alignment: out_scale 4 bytes, everything else 16.                          */
 int dfs_norm_q8(const void* x, const void* residual, const void* weight, dfs_dtype_t dt, int64_t rows, int64_t d,
                 double eps, uint8_t* out_q, float* out_scale, void* out_total, void* out_norm, hipStream_t stream);
 

@@ -25,3 +25,19 @@ def test_the_smallest_and_the_largest_scale(dfs, T, group):
     for scale in (1e-46, 2.4e38):
         with pytest.raises(dfs.DfsError):
             dfs.tree_attention(*a, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_the_smallest_and_the_largest_eps(dfs, dtype):
+    """A row of zeros stays zero with the smallest positive eps, and any row is zero under the largest."""
+    x, w = torch.zeros(3, 256, device="cuda", dtype=dtype), torch.ones(256, device="cuda", dtype=dtype)
+    x[1] = 1.0
+    for eps in (2.0 ** -149, 1e-39, 3.4e38):
+        q, scale, y = dfs.norm_q8(x, w, eps=eps, normed=True)
+        want = 1.0 if eps < 1 else (1.0 + eps) ** -0.5
+        rel = torch.finfo(dtype).eps / 2 + 50 * 2.0 ** -24  # the output's rounding, the norm's own
+        assert (q[[0, 2]].float() == 0).all() and (scale[:, [0, 2]] == 2.0 ** -100).all()
+        assert ((y[1].double() - want).abs() <= rel * want).all()
+    for eps in (1e-46, 3.5e38):
+        with pytest.raises(dfs.DfsError):
+            dfs.norm_q8(x, w, eps=eps)

@@ -16,3 +16,14 @@ def test_a_scale_outside_fp32_is_refused(L):  # noqa: F811
         assert f(scale) == E_ARG, scale
     for scale in (FP32_TINY, 1e-30, 1.0, 2.3e38):
         assert passes(f, scale), scale
+
+
+def test_an_eps_outside_fp32_is_refused(L):  # noqa: F811
+    """The kernel adds fp32(eps): a positive one may not become zero, nor a finite one infinite."""
+    def f(eps):
+        return L.dfs_norm_q8(P, None, P + (2 << 32), 1, 4, 256, eps, FAR, FAR + (1 << 32), None, None, None)
+
+    for eps in (1e-300, FP32_TINY / 4, 3.5e38, 1e300):
+        assert f(eps) == E_ARG, eps
+    for eps in (0.0, FP32_TINY, 1e-6, FP32_MAX):
+        assert passes(f, eps), eps
