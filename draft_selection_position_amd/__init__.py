@@ -527,7 +527,6 @@ def lmhead_logits(hidden: torch.Tensor, W_lm: torch.Tensor, out: torch.Tensor | 
 # checked on every call is one attribute each; the words for a refusal are found afterwards.
 
 _CODES = {torch.float32: F32, torch.bfloat16: BF16}
-_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _fits(t, dtype, index: int) -> bool:
@@ -551,11 +550,12 @@ def _refuse(first: str, tensors: dict, dtypes: dict) -> None:
 
 def _call(index: int, where: str, fn, *args) -> None:
     """fn(*args, stream) on HIP device `index` and its current stream."""
+    stream = torch._C._cuda_getCurrentRawStream(index)  # looked up here: a CPU build of torch has no such name
     if index == torch.cuda.current_device():
-        rc = fn(*args, _raw_stream(index))
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(index):
-            rc = fn(*args, _raw_stream(index))
+            rc = fn(*args, stream)
     if rc != 0:
         raise DfsError(rc, where)
 

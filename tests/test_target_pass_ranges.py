@@ -1,5 +1,7 @@
-"""Arguments of the verification pass's operators at the ends of their ranges (CPU)."""
+"""Arguments of the verification pass's operators at the ends of their ranges, and the package's import (CPU)."""
 import ctypes
+import subprocess
+import sys
 
 from .test_target_pass_oracle import E_ARG, FAR, L, P, _shape, passes  # noqa: F401
 
@@ -27,3 +29,15 @@ def test_an_eps_outside_fp32_is_refused(L):  # noqa: F811
         assert f(eps) == E_ARG, eps
     for eps in (0.0, FP32_TINY, 1e-6, FP32_MAX):
         assert passes(f, eps), eps
+
+
+def test_imports_where_torch_has_no_gpu_streams():
+    """As in a CPU build of torch, which lacks the call that gives a device's current stream."""
+    code = ("import torch\n"
+            "if hasattr(torch._C, '_cuda_getCurrentRawStream'): del torch._C._cuda_getCurrentRawStream\n"
+            "import draft_selection_position_amd as dfs\n"
+            "x = torch.zeros(2, 256)\n"
+            "try:\n    dfs.norm_q8(x, x[0])\nexcept ValueError as e:\n    print(e)\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    assert "HIP device" in r.stdout
