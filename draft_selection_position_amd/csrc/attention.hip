@@ -418,7 +418,8 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
     if (a.pieces && first == 0 && head == 0 && rt == 0 && threadIdx.x == 0)
       a.pieces[seq] = make_int2(g, (int)(((double)(before + tiles) * (double)parts - 1.0) / (double)total));
     const int n = last - first;  // steps
-    const int32_t* table = a.c.block_table + (int64_t)seq * a.c.table_width;
+    // nothing cached: no entry of the table counts, and look-ups read the length (unused) in its place
+    const int32_t* table = len > 0 ? a.c.block_table + (int64_t)seq * a.c.table_width : a.c.lens + seq;
     // Pages of a step's keys or more: they lie in one, read by a scalar load a step ahead.
     const bool wide = (1 << a.c.page_shift) >= C::kKeys;
     auto wide_page = [&](int i) {

@@ -7,7 +7,7 @@ Tolerances are the product's (see test_gpu_target_pass); tests on one value a ro
 import pytest
 import torch
 
-from .test_gpu_target_pass import dfs, gen  # noqa: F401
+from .test_gpu_target_pass import U, dfs, gen, quantised  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -44,6 +44,27 @@ def in_64_bits(a, sa, w, sw):
     return out, mag
 
 
+def bound(mag, want, rows, N, K, dtype):
+    """The product's tolerance: the 8-bit instruction's loss for a bf16 output in tiles, else fp32 sums, and half a
+    step of the output."""
+    tiles = rows > 32 or (rows > 16 and N >= 16384 and K > 24 * 128)
+    lost = 2.0 ** -10 if dtype == torch.bfloat16 and tiles else (256 + 2 * -(-K // 128) + 12) * U
+    return lost * mag + torch.finfo(dtype).eps / 2 * want.abs() + 1e-38
+
+
+@pytest.mark.parametrize("rows,N,K", STREAM + WIDE + FEW[2:3] + TALL[1:] + SMALL[:1])
+def test_accuracy(dfs, rows, N, K):
+    g = gen(rows + N + K)
+    a, sa = quantised(g, rows, K, 1)
+    sa = sa.t().contiguous()
+    w, sw = quantised(g, N, K, 128, 0.05)
+    want, mag = in_64_bits(a, sa, w, sw)
+    for dtype in DTYPES:
+        got = dfs.linear_q8(a, sa, w, sw, out_dtype=dtype).double()
+        far = ((got - want).abs() / bound(mag, want, rows, N, K, dtype)).max().item()
+        assert far <= 1, (dtype, far)
+
+
 def one_value_a_row(g, rows, N, K):
     """Row r of a has one value, 1, at a k of its own, so that out is w's code there times two powers of two: exact,
     in fp32 and in bf16.  w holds every code but the two NaN."""
@@ -65,6 +86,15 @@ def same(got, want):
 
 
 @pytest.mark.parametrize("rows,N,K", ALL)
+def test_every_code(dfs, rows, N, K):
+    a, sa, w, sw, at = one_value_a_row(gen(rows + K), rows, N, K)
+    col = torch.arange(N, device="cuda")
+    want = w.float()[:, at].t() * sa[at // 128, torch.arange(rows, device="cuda")][:, None] * sw[col // 128][:, at // 128].t()
+    for dtype in DTYPES:
+        assert same(dfs.linear_q8(a, sa, w, sw, out_dtype=dtype).float(), want), dtype
+
+
+@pytest.mark.parametrize("rows,N,K", ALL)
 def test_infinite_scales(dfs, rows, N, K):
     """An infinite scale of the last block of k, or of a block of columns there: infinite, with the product's sign,
     where the definition is, and NaN only where it is (zero times infinity)."""
@@ -80,3 +110,43 @@ def test_infinite_scales(dfs, rows, N, K):
         for dtype in DTYPES:
             got = dfs.linear_q8(a, sa2, w, sw2, out_dtype=dtype).double()
             assert same(got, want), (side, dtype, int(torch.isnan(got).sum()), int(torch.isnan(want).sum()))
+
+
+@pytest.mark.parametrize("rows,N,K", ALL)
+def test_nan_stays_in_its_row_and_column(dfs, rows, N, K):
+    g = gen(N + K)
+    a, sa = quantised(g, rows, K, 1)
+    sa = sa.t().contiguous()
+    w, sw = quantised(g, N, K, 128)
+    r, n = rows // 2, N - 1
+    a2, w2 = a.clone(), w.clone()
+    a2.view(torch.uint8)[r, K - 1] = 0x7F
+    w2.view(torch.uint8)[n, K - 16] = 0xFF
+    for dtype in DTYPES:
+        clean = dfs.linear_q8(a, sa, w, sw, out_dtype=dtype)
+        got = dfs.linear_q8(a2, sa, w2, sw, out_dtype=dtype)
+        assert torch.isnan(got[r]).all() and torch.isnan(got[:, n]).all()
+        got[r], got[:, n] = clean[r], clean[:, n]
+        assert torch.equal(got.view(torch.uint8), clean.view(torch.uint8)), dtype
+
+
+@pytest.mark.parametrize("rows,N,K", [(16, 300, 272), (32, 16400, 272), (33, 16400, 272), (100, 300, 272), (333, 5003, 272),
+                                     (512, 5125, 272), (1000, 5003, 272), (2049, 7001, 272)])
+def test_large_products_that_cancel(dfs, rows, N, K):
+    """448 * 448 and its negative among every eight products.  With an fp32 output, and where rows are few, the sums are
+    fp32's; in tiles with a bf16 output a sum is within 2^-10 of the magnitudes, which here is more than what is left."""
+    g = gen(K + rows)
+    a = torch.randn(rows, K, generator=g, device="cuda")
+    w = torch.randn(N, K, generator=g, device="cuda")
+    a[:, 1::8], a[:, 6::8] = 448.0, 448.0
+    w[:, 1::8], w[:, 6::8] = 448.0, -448.0
+    a, w = a.to(torch.float8_e4m3fn), w.to(torch.float8_e4m3fn)
+    G = -(-K // 128)
+    sa, sw = torch.ones(G, rows, device="cuda"), torch.ones(-(-N // 128), G, device="cuda")
+    want, mag = in_64_bits(a, sa, w, sw)
+    for dtype in DTYPES:
+        err = (dfs.linear_q8(a, sa, w, sw, out_dtype=dtype).double() - want).abs()
+        far = (err / bound(mag, want, rows, N, K, dtype)).max().item()
+        print(f"rows {rows} {dtype}: largest error / magnitudes {(err / mag).max().item():.3e}, rms error / rms "
+              f"{(err.square().mean() / want.square().mean()).sqrt().item():.3e}", flush=True)
+        assert far <= 1, (dtype, far)
