@@ -622,7 +622,8 @@ def linear_q8(q: torch.Tensor, scale: torch.Tensor, W: torch.Tensor, W_scale: to
     """The product of e4m3 operands with a scale for each block of 128 (see dfs_linear_q8): [..., N].
 
     q [..., K] e4m3 with scale [ceil(K / 128), rows] fp32 (``norm_q8``'s); W [N, K] e4m3 with W_scale
-    [ceil(N / 128), ceil(K / 128)] fp32.  ``out_dtype`` bf16 or fp32."""
+    [ceil(N / 128), ceil(K / 128)] fp32.  ``out_dtype`` bf16 or fp32.  With bf16 and more than 16 rows sums may be
+    off by 2^-10 of their products' magnitudes, which shows where large ones cancel; never with fp32."""
     e4m3, f32 = torch.float8_e4m3fn, torch.float32
     index = q.get_device() if isinstance(q, torch.Tensor) else -1
     if not (_fits(q, e4m3, index) and _fits(scale, f32, index) and _fits(W, e4m3, index)

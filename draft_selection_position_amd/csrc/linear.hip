@@ -47,9 +47,11 @@ struct LinearArgs {
 
 // The 16 x 16 sums of one block of 128 k, from zero.  A lane holds 32 k of a row of w and of a.
 //
-// kExact false: V_MFMA_F32_16X16X128_F8F6F4 on the e4m3 values.  It aligns the block's
-// products to the largest and loses what is far below it, so its sums are off by about
-// 2e-5 (2-norm, relative), which a bf16 output (2^-8) does not show and an fp32 output does.
+// kExact false: V_MFMA_F32_16X16X128_F8F6F4 on the e4m3 values.  It aligns every eight products
+// of neighbouring k to the largest of them and cuts each off at 2^-13 of it (measured, one value
+// at a time), then adds as in fp32: at most 7 x 2^-13 of each eight's largest is lost, 2e-5 (2-norm,
+// relative) of normally distributed data, which a bf16 output (2^-8) does not show and an fp32 one
+// does.  Where large products cancel it is more than what is left, in either output.
 // kExact true: the values widened to bf16 (exact) through V_MFMA_F32_16X16X32_BF16, whose
 // sums are fp32 sums, at half the rate.
 template <bool kExact>

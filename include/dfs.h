@@ -353,10 +353,14 @@ int dfs_norm_q8(const void* x, const void* residual, const void* weight, dfs_dty
 
 /* ---------------------------------------------------------------- 8-bit product
  * out[r, n] = sum_g a_scale[g, r] w_scale[n / 128, g] sum_{k in group g} a[r, k] w[n, k]
- * over groups g of 128 k (the last may be shorter), out rounded once.  Sums in fp32; for
- * out_dt DFS_BF16, but for few rows, a group's products go through the 8-bit matrix instruction,
- * which loses what is 2^13 below the largest of eight neighbouring products (about 2e-5 of
- * the result's 2-norm: a hundredth of the output's own rounding).  With w an LM head these are the logits that dfs_topk, dfs_select and dfs_verify read.
+ * over groups g of 128 k (the last may be shorter), out rounded once.  Sums and the scales'
+ * product in fp32.  For out_dt DFS_BF16 and more than 16 rows a group's products may go through
+ * the 8-bit matrix instruction, which aligns every eight neighbouring products to the largest of
+ * them and drops each one's part below 2^-13 of it: at most 2^-10 sum |a w| scales in all.  On
+ * normally distributed data that is 2e-5 of the result's 2-norm; where large products cancel, what
+ * is left may be lost whole, and a row may come out otherwise among few rows than among many.
+ * An fp32 output is never computed so.  With w an LM head these are the logits that dfs_topk,
+ * dfs_select and dfs_verify read.
  *   a [rows, K], w [N, K] e4m3 (OCP); a_scale [ceil(K / 128), rows] (dfs_norm_q8's order) and
  *   w_scale [ceil(N / 128), ceil(K / 128)] fp32; out [rows, N] of dtype out_dt, not overlapping an
  *   input.

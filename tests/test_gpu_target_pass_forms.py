@@ -128,3 +128,25 @@ def test_nan_stays_in_its_row_and_column(dfs, rows, N, K):
         assert torch.isnan(got[r]).all() and torch.isnan(got[:, n]).all()
         got[r], got[:, n] = clean[r], clean[:, n]
         assert torch.equal(got.view(torch.uint8), clean.view(torch.uint8)), dtype
+
+
+@pytest.mark.parametrize("rows,N,K", [(16, 300, 272), (32, 16400, 272), (33, 16400, 272), (100, 300, 272), (333, 5003, 272),
+                                     (512, 5125, 272), (1000, 5003, 272), (2049, 7001, 272)])
+def test_large_products_that_cancel(dfs, rows, N, K):
+    """448 * 448 and its negative among every eight products.  With an fp32 output, and where rows are few, the sums are
+    fp32's; in tiles with a bf16 output a sum is within 2^-10 of the magnitudes, which here is more than what is left."""
+    g = gen(K + rows)
+    a = torch.randn(rows, K, generator=g, device="cuda")
+    w = torch.randn(N, K, generator=g, device="cuda")
+    a[:, 1::8], a[:, 6::8] = 448.0, 448.0
+    w[:, 1::8], w[:, 6::8] = 448.0, -448.0
+    a, w = a.to(torch.float8_e4m3fn), w.to(torch.float8_e4m3fn)
+    G = -(-K // 128)
+    sa, sw = torch.ones(G, rows, device="cuda"), torch.ones(-(-N // 128), G, device="cuda")
+    want, mag = in_64_bits(a, sa, w, sw)
+    for dtype in DTYPES:
+        err = (dfs.linear_q8(a, sa, w, sw, out_dtype=dtype).double() - want).abs()
+        far = (err / bound(mag, want, rows, N, K, dtype)).max().item()
+        print(f"rows {rows} {dtype}: largest error / magnitudes {(err / mag).max().item():.3e}, rms error / rms "
+              f"{(err.square().mean() / want.square().mean()).sqrt().item():.3e}", flush=True)
+        assert far <= 1, (dtype, far)
