@@ -611,7 +611,6 @@ def norm_q8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None
     return (q, scale, total_out, y) if normed else (q, scale, total_out)
 
 
-@functools.lru_cache(maxsize=1024)
 def linear_q8_workspace_bytes(rows: int, N: int, K: int) -> int:
     return int(lib().dfs_linear_q8_workspace_bytes(rows, N, K))
 
@@ -623,7 +622,8 @@ def linear_q8(q: torch.Tensor, scale: torch.Tensor, W: torch.Tensor, W_scale: to
 
     q [..., K] e4m3 with scale [ceil(K / 128), rows] fp32 (``norm_q8``'s); W [N, K] e4m3 with W_scale
     [ceil(N / 128), ceil(K / 128)] fp32.  ``out_dtype`` bf16 or fp32.  With bf16 and more than 16 rows sums may be
-    off by 2^-10 of their products' magnitudes, which shows where large ones cancel; never with fp32."""
+    off by 2^-10 of their products' magnitudes, which shows where large ones cancel; never with fp32.
+    ``workspace`` is not used: no size needs any."""
     e4m3, f32 = torch.float8_e4m3fn, torch.float32
     index = q.get_device() if isinstance(q, torch.Tensor) else -1
     if not (_fits(q, e4m3, index) and _fits(scale, f32, index) and _fits(W, e4m3, index)
@@ -644,10 +644,8 @@ def linear_q8(q: torch.Tensor, scale: torch.Tensor, W: torch.Tensor, W_scale: to
         out = scale.new_empty(shape[:-1] + (N,), dtype=out_dtype)
     elif out.shape != shape[:-1] + (N,):
         raise ValueError("out must be [..., N]")
-    nb = linear_q8_workspace_bytes(rows, N, K)
-    ws = _scratch(workspace, q, nb)
     _call(index, "dfs_linear_q8", lib().dfs_linear_q8, q.data_ptr(), scale.data_ptr(), W.data_ptr(), W_scale.data_ptr(),
-          rows, N, K, _CODES[out_dtype], out.data_ptr(), _ptr(ws), nb)
+          rows, N, K, _CODES[out_dtype], out.data_ptr(), None, 0)
     return out
 
 

@@ -611,8 +611,8 @@ static int check_linear_q8_shape(int64_t rows, int64_t N, int64_t K) {
 }
 
 size_t dfs_linear_q8_workspace_bytes(int64_t rows, int64_t N, int64_t K) {
-  if (check_linear_q8_shape(rows, N, K) != DFS_OK) return 0;
-  return linear_q8_workspace_bytes(rows, N, K);
+  (void)rows, (void)N, (void)K;
+  return 0;  // no size needs any
 }
 
 int dfs_linear_q8(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale, int64_t rows,
@@ -628,12 +628,11 @@ int dfs_linear_q8(const uint8_t* a, const float* a_scale, const uint8_t* w, cons
   if (overlaps(out, on, a, (size_t)(rows * K)) || overlaps(out, on, w, (size_t)(N * K)) ||
       overlaps(out, on, a_scale, G * rows * 4) || overlaps(out, on, w_scale, G * cdiv(N, 128) * 4))
     return DFS_E_ARG;
-  const size_t need = linear_q8_workspace_bytes(rows, N, K);
-  if (need > 0 && (!ws || ws_bytes < need)) return DFS_E_WORKSPACE;
   if (ws && !aligned(ws, 256)) return DFS_E_ALIGN;
+  (void)ws_bytes;
   if ((st = check_device()) != DFS_OK) return st;
   (void)hipGetLastError();
-  return hip_status(launch_linear_q8(a, a_scale, w, w_scale, rows, N, K, out_dt == DFS_BF16, out, ws, stream));
+  return hip_status(launch_linear_q8(a, a_scale, w, w_scale, rows, N, K, out_dt == DFS_BF16, out, stream));
 }
 
 // What the cache's shape must be for either call on it.

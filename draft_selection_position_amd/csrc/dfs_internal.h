@@ -199,10 +199,8 @@ hipError_t launch_norm_q8(const void* x, const void* residual, const void* weigh
                           float eps, uint8_t* q, float* scale, void* total, void* normed, hipStream_t stream);
 
 // ---------------------------------------------------------------- 8-bit product
-size_t linear_q8_workspace_bytes(int64_t rows, int64_t N, int64_t K);
 hipError_t launch_linear_q8(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale,
-                            int64_t rows, int64_t N, int64_t K, bool bf16_out, void* out, void* ws,
-                            hipStream_t stream);
+                            int64_t rows, int64_t N, int64_t K, bool bf16_out, void* out, hipStream_t stream);
 
 // ---------------------------------------------------------------- paged cache
 // Pages [n_pages, kv_heads, page rows, row_bytes] of K and of V, and who owns which.

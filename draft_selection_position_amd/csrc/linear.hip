@@ -656,11 +656,8 @@ hipError_t launch_linear(const LinearArgs& p, hipStream_t stream) {
 
 }  // namespace
 
-size_t linear_q8_workspace_bytes(int64_t rows, int64_t N, int64_t K) { return 0; }
-
 hipError_t launch_linear_q8(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale,
-                            int64_t rows, int64_t N, int64_t K, bool bf16_out, void* out, void* ws,
-                            hipStream_t stream) {
+                            int64_t rows, int64_t N, int64_t K, bool bf16_out, void* out, hipStream_t stream) {
   const LinearArgs p{a, a_scale, w, w_scale, out, rows, N, (int)K, (int)cdiv(K, kBlock)};
   return bf16_out ? launch_linear<true>(p, stream) : launch_linear<false>(p, stream);
 }

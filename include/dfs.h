@@ -366,8 +366,7 @@ int dfs_norm_q8(const void* x, const void* residual, const void* weight, dfs_dty
  *   input.
  * K a multiple of 16 in [16, DFS_MAX_D], 1 <= N < 2^31, 1 <= rows <= DFS_MAX_ROWS and
  * ceil(rows / 64) * ceil(N / 64) <= 2^23, N * K <= 2^39.  Alignment: a, w, out 16 bytes; scales 4; ws 256.
- * ws: dfs_linear_q8_workspace_bytes(rows, N, K) bytes of scratch (may be 0, then ws may be
- * NULL).                                                                           */
+ * No size needs scratch memory: the query gives 0, ws may be NULL and is not used.  */
 size_t dfs_linear_q8_workspace_bytes(int64_t rows, int64_t N, int64_t K);
 int dfs_linear_q8(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale, int64_t rows,
                   int64_t N, int64_t K, dfs_dtype_t out_dt, void* out, void* ws, size_t ws_bytes,
