@@ -11,8 +11,9 @@
 // 32 away, a rescale is one factor per lane, and P^T's registers are already the second
 // product's operand (its 16 keys per instruction are taken in the order in which S^T's
 // sums lie; V^T comes out of LDS in the same order by the transposing read).  P is rounded
-// to bf16 for the matrix cores (relative 2^-8 per weight, as the output's own rounding);
-// scores, maxima, sums and O stay in fp32.
+// to bf16 for the matrix cores (at most 2^-8 per weight, as the output's own rounding; the sums of
+// weights take them as they were): 2-norm errors of 0.0018 to 0.0023 against 0.0016 of the output's
+// rounding alone.  Scores, maxima, sums and O stay in fp32.
 //
 // K and V tiles go from memory straight into LDS, through a ring of stages.  Up to 32 query
 // rows: four waves take tiles of 32 keys of their own and never wait for each other until they
@@ -24,9 +25,9 @@
 // from fp32 partial results.  A sequence's nodes are keys like the cache's, right behind them.
 //
 // What bounds it (MI355X): 64 sequences of 17 nodes, 4 heads to a kv head of 128, 0 to 8192 cached
-// keys: 205 us, memory at 5.3 TB/s.  2 x 64 nodes x 6 heads to a kv head of 64, 131001 keys: 142 to
-// 148 us, 700 TFLOP/s; a head of 64 costs as many exponentials as products' cycles, and the
-// card holds 2.0 GHz under it.  One token, 4001 keys: 11.8 us, two launches and a chain of four
+// keys: 205 to 209 us, memory at 5.3 TB/s.  2 x 64 nodes x 6 heads to a kv head of 64, 131001 keys: 144 to
+// 149 us, 700 TFLOP/s; a head of 64 costs as many exponentials as products' cycles, and the
+// card holds 2.0 GHz under it.  One token, 4001 keys: 12.0 us, two launches and a chain of four
 // memory latencies (lengths, pages, keys, pieces); its 16 MB would take 2.5.
 #include "dfs_device.h"
 #include "dfs_internal.h"
@@ -147,8 +148,7 @@ __device__ __forceinline__ int seq_tiles(const AttnArgs& a, int b) {
 }
 
 // Parts that `total` tiles are cut into: from 32 a sequence on of four tiles or more, as the join reads every
-// row once for each (68 rows of 128, 4001 keys: 20.4 us against 23.0; 84 of 64, 2 x 23520: 24.9, and 32
-// without this by three waves a workgroup).
+// row once for each (68 rows of 128, 4001 keys: 20.4 us against 23.0).
 __device__ __forceinline__ int parts_of(const AttnArgs& a, int total) {
   return min(min(a.G, total), max(32 * a.batch, (total + 3) / 4));
 }
@@ -652,8 +652,9 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
 
 // Sequences cut over several workgroups: their pieces joined.  16 lanes hold a row's D
 // values and take every `spread`-th of its pieces, two at a time, statistics and values in
-// one go, so that a row takes one memory latency or two however many pieces it has: 16
-// rows a workgroup for few pieces (spread 1), 4 for more (a wave a row), or one.
+// one go: ceil(pieces / (2 spread)) rounds of memory latency for a row.  16 rows a workgroup for few
+// pieces (spread 1), 4 for more (a wave a row), or one; by the parts for each sequence on average, so
+// a long sequence among many short ones takes more rounds than it would have to.
 template <class C>
 __global__ __launch_bounds__(256) void tree_attention_join_kernel(AttnArgs a) {
   constexpr int kPer = C::D / 16;  // values of a lane
@@ -775,7 +776,9 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
 // against 32 keys and four (a barrier for every 16 KB): 203 us against 217 at 64 sequences x 17
 // nodes x 8192 keys, head 128; 147 against 162 at 2 x 64 nodes x 131001 keys, head 64.  65 to 96 rows of
 // 128: three waves (211 us against 214 by four at 64 x 17 nodes x 8192 keys); of 64: four, an idle one
-// among them (122 against 145: by three, twelve waves on a CU, the registers do not suffice).
+// among them (120 against 144: by three, twelve waves on a CU, the registers do not suffice; of 18 more
+// sizes all gain, 2 x 28 nodes x 3 heads x 23520 keys 16.6 against 17.5, 64 x 17 nodes x 5 heads x 1000 keys
+// 28.3 against 36.8).
 template <int D, class F>
 auto with_cfg(int64_t rows, F f) {
   if (rows <= 32) return f(Cfg<D, 4, 1, D == 64 ? 3 : 2, 1>{});
@@ -798,7 +801,8 @@ AttnPlan plan_tree_attention(const CacheView& c, int64_t batch, int64_t T, int64
     const int64_t each = cdiv(((int64_t)c.table_width << c.page_shift) + T, (int64_t)C::kTile), most = batch * each;
     p.G = 256 * C::kGroups / (p.row_tiles * c.kv_heads);
     p.G = p.G < 1 ? 1 : p.G > most ? most : p.G;
-    // Few tiles a sequence at most: a part for each and no join (4 x 9 nodes, page 256: 8.0 us
+    // Few tiles a sequence at most, by the table's width (the lengths are on the device: a table for more
+    // keys cuts sequences however short they are): a part for each and no join (4 x 9 nodes, page 256: 8.0 us
     // against 10.2; 39 x 33 nodes, up to 61 keys: 17.8 against 24.4; 13 x 56 nodes, 7 heads, 243 keys: 16.2
     // against 27.9; at worst 2 x 18 nodes, 3 heads, 115 keys: 14.0 against 12.8).
     p.whole = each <= 4 || (each <= 8 && batch * c.kv_heads * p.row_tiles >= 48);

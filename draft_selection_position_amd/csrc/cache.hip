@@ -4,7 +4,7 @@
 // lens[b] + i of the sequence, page block_table[b, position / page], row position % page.
 // Pure data movement, bound by memory (or by the launch, for few tokens): one workgroup
 // per accepted token moves its K and V rows of all heads, 16 bytes per lane; a row of one
-// head is contiguous on both sides.  One sequence's tokens: 2.0 us on the device, the launch;
+// head is contiguous on both sides.  One sequence's tokens: 2.4 us on the device, the launch;
 // 256 sequences', up to 33 each, 8 heads of 128: 6.4 us for 18 MB read and written, one round
 // of workgroups that each wait for counts, lengths, page and rows in turn.
 #include "dfs_device.h"

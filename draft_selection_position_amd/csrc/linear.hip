@@ -14,10 +14,10 @@
 // c ^ ((row >> 1) & 7): the 16 rows that a fragment read touches then fall on distinct
 // banks.  Rows and k past the end of an operand read as zeros.
 //
-// What bounds it (MI355X): 4096 x 151936 x 5120, 2950 us, 2150 TFLOP/s: 64 KB a step into each
+// What bounds it (MI355X): 4096 x 151936 x 5120, 2920 to 3020 us, 2110 to 2180 TFLOP/s: 64 KB a step into each
 // CU's LDS, which alone take 2240 us (18 bytes a clock, also where all of it hits the L2);
 // products and LDS reads without them take 1990.  Through registers instead they alone take
-// 1500, but the step as a whole is no faster for it (3050).  One row of 5120 x 4096, 6.6 us, and 16
+// 1500, but the step as a whole is no faster for it (3050).  One row of 5120 x 4096, 6.8 to 7.1 us, and 16
 // of 151936 x 5120, 138 to 148: reading w.
 #include "dfs_device.h"
 #include "dfs_internal.h"
@@ -615,13 +615,13 @@ hipError_t launch_stream(const LinearArgs& p, hipStream_t stream) {
 
 // Which kernel (times in us, bf16 output unless said, by rows x N x K):
 //   up to 16 rows  the streaming kernel from 16384 columns on, up to K = 5120 (16 x 151936 x 5120,
-//                  fp32: 138 against 175), else the one for few rows (1 x 5120 x 4096: 6.6)
+//                  fp32: 138 against 175), else the one for few rows (1 x 5120 x 4096: 6.8 to 7.1)
 //   up to 32 rows  the same, the streaming one up to 24 blocks of k (its fragments of a spill
 //                  beyond; 32 x 5120 x 4096: 9.9 against 11.3 in tiles)
 //   up to 64 rows  128 x 64 tiles from 16384 columns on (64 x 151936 x 5120: 153 against 177 in
 //                  64 x 64), else as for more
 //   more           256 x 256 tiles, one to a CU, or 128 x 128 from 300 on, two to a CU (1024 x 10240 x
-//                  5120: 82 against 108 in 64 x 64), by their rounds: a round of the large ones
+//                  5120: 82 against 108 in 64 x 64, and 66 in 256 x 256), by their rounds: a round of the large ones
 //                  takes 1600 / 1024 of a round of the others, whose last, if short, takes half of
 //                  one and half of its share (4096 x 151936 x 5120: 2950 against 3590; 4096 x 4096 x
 //                  4096: 69 against 85; 1024 x 65536 x 2048: 156 against 199; 2048 x 5120 x 5120, 640

@@ -6,7 +6,7 @@
 // One pass over the data: a row is read once into registers (8 values per lane per step),
 // the sum of squares is reduced over its waves, and a group's 128 values are 16
 // neighbouring lanes, so its largest value is four DPP steps.  Bound by memory: 16320 x 5120 bf16
-// with a residual, 109.5 us, 5.4 TB/s; 16 rows, 4.4 us on the device.  s stays in fp32 from the
+// with a residual, 112 us, 5.3 TB/s; 16 rows, 4.7 us on the device.  s stays in fp32 from the
 // addition to the quantisation: the rounded sum that later layers read (out_total) is not
 // what is normalised.
 //
