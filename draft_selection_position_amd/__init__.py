@@ -27,7 +27,8 @@ __all__ = [
     "select", "Selector", "select_workspace_bytes", "topk_workspace_bytes", "PackedWeight", "gate_pack",
     "gate_workspace_bytes", "status_str", "conv2", "conv2_workspace_bytes", "Conv2", "lmhead_topk", "lmhead_logits",
     "lmhead_topk_workspace_bytes", "norm_q8", "linear_q8", "linear_q8_workspace_bytes", "tree_attention",
-    "tree_attention_workspace_bytes", "cache_commit",
+    "tree_attention_workspace_bytes", "cache_commit", "tree_positions", "rope_frequencies", "rope", "cache_append",
+    "tree_attention_shared", "tree_attention_shared_workspace_bytes",
 ]
 
 K = 16
@@ -57,6 +58,12 @@ class _Shape(ctypes.Structure):
 class _CacheShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("batch", "T", "q_heads", "kv_heads", "head_dim", "page_size",
                                               "n_pages", "table_width")] + [("dtype", ctypes.c_int)]
+
+
+class _RopeShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "q_heads", "kv_heads", "head_dim", "rot_dim", "q_stride",
+                                              "k_stride", "v_stride")] + [
+        ("amplitude", ctypes.c_double), ("layout", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
 def lib() -> ctypes.CDLL:
@@ -131,6 +138,20 @@ def lib() -> ctypes.CDLL:
         L.dfs_tree_attention.restype = c_int
         L.dfs_cache_commit.argtypes = [vp, vp, i32p, i32p, i64, vp, vp, i32p, i32p, cache, i32p, vp]
         L.dfs_cache_commit.restype = c_int
+        L.dfs_tree_positions.argtypes = [i32p, i32p, i32p, i64, i64, i32p, vp]
+        L.dfs_tree_positions.restype = c_int
+        L.dfs_rope_frequencies.argtypes = [i64, c_double, c_int, c_double, c_double, c_double, c_double, vp, vp]
+        L.dfs_rope_frequencies.restype = c_int
+        rope = ctypes.POINTER(_RopeShape)
+        L.dfs_rope.argtypes = [vp, vp, vp, i32p, f32p, rope, vp, vp, vp, vp]
+        L.dfs_rope.restype = c_int
+        L.dfs_cache_append.argtypes = [vp, vp, vp, i32p, f32p, rope, i32p, vp, vp, vp, i32p, i32p, cache, i32p, vp]
+        L.dfs_cache_append.restype = c_int
+        L.dfs_tree_attention_shared_workspace_bytes.argtypes = [cache, i64]
+        L.dfs_tree_attention_shared_workspace_bytes.restype = sz
+        L.dfs_tree_attention_shared.argtypes = [vp, vp, vp, i32p, vp, vp, i32p, i32p, i64, i32p, i32p, cache, c_double,
+                                                vp, vp, sz, vp]
+        L.dfs_tree_attention_shared.restype = c_int
         _lib = L
     return _lib
 
@@ -748,6 +769,255 @@ def cache_commit(k_new: torch.Tensor, v_new: torch.Tensor, nodes: torch.Tensor |
           counts.data_ptr(), path, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), lens.data_ptr(), s,
           out_lens.data_ptr())
     return out_lens
+
+
+def tree_positions(parents: torch.Tensor, lens: torch.Tensor, prefix_len: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """Positions of a drafted tree's nodes, for ``rope`` (see dfs_tree_positions): int32 [batch, T].
+
+    parents [batch, T] int32 (as for ``tree_attention``), lens [batch] int32, prefix_len [1] int32: tokens that a
+    shared prefix puts in front of every sequence's own."""
+    i32 = torch.int32
+    index = parents.get_device() if isinstance(parents, torch.Tensor) else -1
+    if not (_fits(parents, i32, index) and _fits(lens, i32, index)
+            and (prefix_len is None or _fits(prefix_len, i32, index)) and (out is None or _fits(out, i32, index))):
+        given = {"parents": parents, "lens": lens, "prefix_len": prefix_len, "out": out}
+        given = {k: t for k, t in given.items() if k in ("parents", "lens") or t is not None}
+        _refuse("parents", given, dict.fromkeys(given, i32))
+    shape = parents.shape
+    if len(shape) != 2 or lens.shape != shape[:1]:
+        raise ValueError("parents must be [batch, T] and lens [batch]")
+    if prefix_len is not None and prefix_len.numel() != 1:
+        raise ValueError("prefix_len must be [1]")
+    if out is None:
+        out = torch.empty_like(parents)
+    elif out.shape != shape:
+        raise ValueError("out must have the shape of parents")
+    _call(index, "dfs_tree_positions", lib().dfs_tree_positions, parents.data_ptr(), lens.data_ptr(), _ptr(prefix_len),
+          shape[0], shape[1], out.data_ptr())
+    return out
+
+
+_LAYOUTS = {"half": 0, "interleaved": 1}
+_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                     original: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """(freqs fp32 [rot_dim / 2], amplitude) of a model's rotary positions (see dfs_rope_frequencies), for ``rope``.
+
+    ``scaling`` None, "linear", "ntk", "yarn" or "bands"; ``original``: the positions that the model was trained
+    on, for the last two ("bands": beta_fast and beta_slow are its high and low frequency factors)."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {list(_SCALINGS)}, got {scaling!r}")
+    freqs = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.float32)
+    amplitude = ctypes.c_double()
+    _check(lib().dfs_rope_frequencies(rot_dim, base, _SCALINGS[scaling], factor, original, beta_fast, beta_slow,
+                                      freqs.data_ptr(), ctypes.byref(amplitude)), "dfs_rope_frequencies")
+    return freqs if device is None else freqs.to(device), amplitude.value
+
+
+def _heads(t, what: str, dtype, index: int):
+    """(rows, heads, head_dim, values from a row to the next) of t [..., heads, head_dim], whose rows may lie apart (a
+    slice of a joint projection's heads), but evenly, and each in one piece."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.get_device() == index):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{what} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{what} must be on a HIP device, got {t.device}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+        raise ValueError(f"{what} must be on cuda:{index}, got {t.device}")
+    shape, step = t.shape, t.stride()
+    if len(shape) < 3:
+        raise ValueError(f"{what} must be [..., heads, head_dim]")
+    H, D = shape[-2:]
+    if not ((step[-1] == 1 or D == 1) and (step[-2] == D or H == 1)):
+        raise ValueError(f"{what}: a token's heads must lie in one piece")
+    rows, apart = 1, H * D
+    for n, by in zip(shape[-3::-1], step[-3::-1]):
+        if n != 1:
+            if rows == 1:
+                apart = by
+            elif by != apart * rows:
+                raise ValueError(f"{what}: rows must lie evenly apart")
+            rows *= n
+    return rows, H, D, apart
+
+
+def _rope_call(q, k, v, freqs, layout, amplitude, dtype, index):
+    """The struct of a call on q, k and v (any of them None), with rows and heads as they are given."""
+    rows = D = None
+    sizes = []
+    for t, what in ((q, "q"), (k, "k"), (v, "v")):
+        if t is None:
+            sizes.append((0, 0))
+            continue
+        n, H, d, apart = _heads(t, what, dtype, index)
+        if rows is None:
+            rows, D = n, d
+        elif (n, d) != (rows, D):
+            raise ValueError(f"{what} must have {rows} tokens and heads of {D}")
+        sizes.append((H, apart))
+    if k is not None and v is not None and k.shape != v.shape:
+        raise ValueError("v must have the shape of k")
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be one of {list(_LAYOUTS)}, got {layout!r}")
+    rot = 0
+    if freqs is not None:
+        if not _fits(freqs, torch.float32, index):
+            _dev(freqs, "freqs", torch.float32)
+            raise ValueError(f"freqs must be on cuda:{index}, got {freqs.device}")
+        if freqs.dim() != 1:
+            raise ValueError("freqs must be [rot_dim / 2]")
+        rot = 2 * freqs.shape[0]
+    (Hq, sq), (Hk, sk), (Hv, sv) = sizes
+    return _RopeShape(rows, Hq, Hk or Hv, D, rot, sq, sk, sv, amplitude, _LAYOUTS[layout], _CODES[dtype])
+
+
+def _rope_dtype(t, what: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a torch.Tensor")
+    if t.dtype not in _CODES:
+        _dtype_code(t, what)
+    return t.dtype, t.get_device()
+
+
+def rope(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None, positions: torch.Tensor,
+         freqs: torch.Tensor, layout: str = "half", amplitude: float = 1.0, out=None):
+    """Rotary positions (see dfs_rope): (q, k, v) with q and k turned and v as it is, dense; None stays None.
+
+    q [..., q_heads, D], k and v [..., kv_heads, D], bf16 or fp32, may be slices of a joint projection's heads, as
+    in ``qkv.view(B, T, -1, D)[:, :, :q_heads]``; positions int32, one for each token (``tree_positions`` for drafted
+    nodes); freqs and amplitude as ``rope_frequencies`` gives them.  ``layout`` "half" or "interleaved".  ``out`` may
+    pass preallocated (q, k, v), which for dense q and k may be these themselves."""
+    lead = q if q is not None else k
+    if lead is None:
+        raise ValueError("q or k must be given")
+    dtype, index = _rope_dtype(lead, "q" if q is not None else "k")
+    if freqs is None:
+        raise TypeError("freqs must be a torch.Tensor")
+    s = _rope_call(q, k, v, freqs, layout, amplitude, dtype, index)
+    if not _fits(positions, torch.int32, index):
+        _dev(positions, "positions", torch.int32)
+        raise ValueError(f"positions must be on cuda:{index}, got {positions.device}")
+    if positions.numel() != s.rows:
+        raise ValueError(f"positions must be one for each of {s.rows} tokens")
+    if out is None:
+        out = tuple(None if t is None else torch.empty(t.shape, dtype=dtype, device=t.device) for t in (q, k, v))
+    else:
+        if len(out) != 3:
+            raise ValueError("out must be (q, k, v)")
+        for t, o, what in zip((q, k, v), out, "qkv"):
+            if (t is None) != (o is None):
+                raise ValueError(f"out must hold {what} if and only if {what} is given")
+            if o is not None and not (_fits(o, dtype, index) and o.shape == t.shape):
+                raise ValueError(f"out's {what} must be a contiguous {dtype} tensor of {what}'s shape on cuda:{index}")
+    oq, ok, ov = out
+    _call(index, "dfs_rope", lib().dfs_rope, _ptr(q), _ptr(k), _ptr(v), positions.data_ptr(), freqs.data_ptr(),
+          ctypes.byref(s), _ptr(oq), _ptr(ok), _ptr(ov))
+    return oq, ok, ov
+
+
+def cache_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor,
+                 freqs: torch.Tensor | None, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+                 lens: torch.Tensor, layout: str = "half", amplitude: float = 1.0,
+                 prefix_len: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                 out_lens: torch.Tensor | None = None):
+    """Puts tokens of several sequences into a paged cache, their keys (and q) turned on the way (see dfs_cache_append).
+
+    k, v [rows, kv_heads, D] and q [rows, q_heads, D] (None: no queries), which may be slices of a joint projection's
+    heads; starts [batch + 1] int32: rows starts[b] .. starts[b + 1] - 1 go behind sequence b's lens[b] tokens.
+    freqs None: nothing is turned.  Writes the pools in place.  Returns (turned q or None, new lengths); rows of
+    q that belong to no sequence are left as ``q_out`` holds them."""
+    i32 = torch.int32
+    dtype, index = _rope_dtype(k, "k")
+    if v is None:
+        raise TypeError("v must be a torch.Tensor")
+    s = _rope_call(q, k, v, freqs, layout, amplitude, dtype, index)
+    if not (_fits(k_pages, dtype, index) and _fits(v_pages, dtype, index) and _fits(starts, i32, index)
+            and _fits(block_table, i32, index) and _fits(lens, i32, index)
+            and (prefix_len is None or _fits(prefix_len, i32, index)) and (q_out is None or _fits(q_out, dtype, index))
+            and (out_lens is None or _fits(out_lens, i32, index))):
+        given = {"k_pages": k_pages, "v_pages": v_pages, "starts": starts, "block_table": block_table, "lens": lens,
+                 "prefix_len": prefix_len, "q_out": q_out, "out_lens": out_lens}
+        given = {n: t for n, t in given.items() if n not in ("prefix_len", "q_out", "out_lens") or t is not None}
+        _refuse("k_pages", given, dict.fromkeys(given, i32) | {"k_pages": dtype, "v_pages": dtype, "q_out": dtype})
+        raise ValueError(f"the pools must be on cuda:{index}, got {k_pages.device}")
+    pages, table = k_pages.shape, block_table.shape
+    if len(pages) != 4 or v_pages.shape != pages or pages[1] != s.kv_heads or pages[3] != s.head_dim:
+        raise ValueError(f"k_pages and v_pages must both be [n_pages, {s.kv_heads}, page_size, {s.head_dim}]")
+    batch = lens.shape[0] if lens.dim() == 1 else -1
+    if len(table) != 2 or table[0] != batch or starts.shape != (batch + 1,):
+        raise ValueError("lens must be [batch], block_table [batch, width] and starts [batch + 1]")
+    if prefix_len is not None and prefix_len.numel() != 1:
+        raise ValueError("prefix_len must be [1]")
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out needs a q")
+    elif q_out is None:
+        q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+    elif q_out.shape != q.shape:
+        raise ValueError("q_out must have the shape of q")
+    if out_lens is None:
+        out_lens = torch.empty_like(lens)
+    elif out_lens.shape != lens.shape:
+        raise ValueError("out_lens must be [batch]")
+    c, _ = _cache_shape(batch, 1, s.kv_heads, s.kv_heads, s.head_dim, pages[2], pages[0], table[1], s.dtype)
+    _call(index, "dfs_cache_append", lib().dfs_cache_append, _ptr(q), k.data_ptr(), v.data_ptr(), starts.data_ptr(),
+          _ptr(freqs), ctypes.byref(s), _ptr(prefix_len), _ptr(q_out), k_pages.data_ptr(), v_pages.data_ptr(),
+          block_table.data_ptr(), lens.data_ptr(), c, out_lens.data_ptr())
+    return q_out, out_lens
+
+
+@functools.lru_cache(maxsize=1024)
+def _shared_scratch(batch, T, q_heads, kv_heads, head_dim, page_size, n_pages, table_width, dt, prefix_width):
+    s, _ = _cache_shape(batch, T, q_heads, kv_heads, head_dim, page_size, n_pages, table_width, dt)
+    return s, int(lib().dfs_tree_attention_shared_workspace_bytes(s, prefix_width))
+
+
+def tree_attention_shared_workspace_bytes(batch: int, T: int, q_heads: int, kv_heads: int, head_dim: int,
+                                          page_size: int, n_pages: int, table_width: int, prefix_width: int) -> int:
+    return _shared_scratch(batch, T, q_heads, kv_heads, head_dim, page_size, n_pages, table_width, BF16, prefix_width)[1]
+
+
+def tree_attention_shared(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, parents: torch.Tensor,
+                          k_pages: torch.Tensor, v_pages: torch.Tensor, prefix_table: torch.Tensor,
+                          prefix_len: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor,
+                          scale: float | None = None, out: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """``tree_attention`` for a batch whose sequences begin with one shared prefix (see dfs_tree_attention_shared).
+
+    prefix_table [width] int32: the prefix's pages in the pools; prefix_len [1] int32.  The other arguments are
+    ``tree_attention``'s, with block_table and lens of what follows the prefix."""
+    bf16, i32 = torch.bfloat16, torch.int32
+    index = q.get_device() if isinstance(q, torch.Tensor) else -1
+    if not (_fits(q, bf16, index) and _fits(parents, i32, index) and isinstance(k_new, torch.Tensor)
+            and _fits(prefix_table, i32, index) and _fits(prefix_len, i32, index)
+            and (out is None or _fits(out, bf16, index))):
+        given = {"q": q, "k_new": k_new, "parents": parents, "prefix_table": prefix_table, "prefix_len": prefix_len}
+        given |= {} if out is None else {"out": out}
+        _refuse("q", given, dict.fromkeys(given, i32) | {"q": bf16, "k_new": bf16, "out": bf16})
+    batch, T, Hkv, D, page, n_pages, width, dt = _cache_sizes(k_new, v_new, k_pages, v_pages, block_table, lens, index)
+    shape = q.shape
+    if len(shape) != 4 or dt != BF16 or shape[0] != batch or shape[1] != T or shape[3] != D:
+        raise ValueError("q must be [batch, T, q_heads, head_dim], with k_new's dtype, batch, T and head_dim")
+    if parents.shape != shape[:2]:
+        raise ValueError("parents must be [batch, T]")
+    if prefix_table.dim() != 1 or prefix_len.numel() != 1:
+        raise ValueError("prefix_table must be [width] and prefix_len [1]")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != shape:
+        raise ValueError("out must have the shape of q")
+    prefix_width = prefix_table.shape[0]
+    s, nb = _shared_scratch(batch, T, shape[2], Hkv, D, page, n_pages, width, dt, prefix_width)
+    ws = _scratch(workspace, q, nb)
+    _call(index, "dfs_tree_attention_shared", lib().dfs_tree_attention_shared, q.data_ptr(), k_new.data_ptr(),
+          v_new.data_ptr(), parents.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), prefix_table.data_ptr(),
+          prefix_len.data_ptr(), prefix_width, block_table.data_ptr(), lens.data_ptr(), s,
+          D ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(ws), nb)
+    return out
 
 
 class Selector:

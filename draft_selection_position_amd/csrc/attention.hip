@@ -29,6 +29,8 @@
 // 149 us, 700 TFLOP/s; a head of 64 costs as many exponentials as products' cycles, and the
 // card holds 2.0 GHz under it.  One token, 4001 keys: 12.0 us, two launches and a chain of four
 // memory latencies (lengths, pages, keys, pieces); its 16 MB would take 2.5.
+#include <algorithm>
+
 #include "dfs_device.h"
 #include "dfs_internal.h"
 #include "mfma_big.h"
@@ -46,6 +48,11 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr float kUnused = -1.0f;  // for a sum of weights
 constexpr float kLag = 8.0f;  // a maximum may lag this far (in powers of two) before sums are rescaled
 
+// What a workgroup's keys are: a sequence's cache and tree, the whole answer; the same of a batch with a shared
+// prefix, whose part of the answer is still to be joined with the prefix's; or the prefix, for the rows of the whole
+// batch as the one sequence that it is (no node is a key then, and every row sees all).
+enum Role { kTree, kOwn, kPrefix };
+
 struct AttnArgs {
   CacheView c;
   const uint16_t* q;
@@ -53,10 +60,16 @@ struct AttnArgs {
   const uint16_t* v_new;
   const int32_t* parents;
   uint16_t* out;
-  float* part_o;   // [Hkv, row tiles, 2 G, rows of a tile, D]
+  float* part_o;   // [Hkv, row tiles, 2 G, rows of a tile, D]; kOwn: 2 G + batch, the last for sequences in one piece
   float* part_ml;  // [Hkv, row tiles, 2 G, rows of a tile, 2]: maximum and sum; of an unused node's row the last piece has kUnused
   int2* pieces;    // [batch]: the first and the last part with a tile of the sequence (NULL: nothing to join)
+  // the shared prefix's pieces: [Hkv, parts, rows of the batch, D] and their maxima and sums, and how many there are
+  float* prefix_o;
+  float* prefix_ml;
+  int* prefix_count;
+  int prefix_G;
   int batch, T, group, G, row_tiles;
+  int nodes;  // of a sequence that are keys: T, or none of the prefix
   bool whole;  // parts are sequences
   int spread;  // 16-lane groups that join a row's pieces: 1, 4 or 16
   float c2;  // scale * log2(e)
@@ -144,7 +157,7 @@ __device__ __forceinline__ uint64_t shfl64(uint64_t x, int src) {
 // Tiles of a sequence: its keys are the cache's and right behind them the tree's.
 template <class C>
 __device__ __forceinline__ int seq_tiles(const AttnArgs& a, int b) {
-  return (a.c.len(b) + a.T + C::kTile - 1) / C::kTile;
+  return (a.c.len(b) + a.nodes + C::kTile - 1) / C::kTile;
 }
 
 // Parts that `total` tiles are cut into: from 32 a sequence on of four tiles or more, as the join reads every
@@ -208,25 +221,6 @@ __device__ __forceinline__ Where locate(const AttnArgs& a, int* scratch, F want)
   }
   __syncthreads();
   return Where{total, scratch[kThreads], scratch[kThreads + 1]};
-}
-
-// The nodes that node `lane` (parent p; none: -2) sees, as bits (none for an unused node):
-// itself and, by doubling along the parents, its ancestors.
-__device__ __forceinline__ uint64_t tree_bits(int p, int T, int lane) {
-  const bool used = p >= -1 && p < lane;
-  uint64_t bits = used ? 1ull << lane : 0;
-  if (!used) p = -1;
-#pragma unroll 1
-  for (int reach = 1; reach < T; reach *= 2) {
-    const int src = p < 0 ? lane : p;
-    const uint32_t lo = __shfl((uint32_t)bits, src), hi = __shfl((uint32_t)(bits >> 32), src);
-    const int pp = __shfl(p, src);
-    if (p >= 0) {
-      bits |= ((uint64_t)hi << 32) | lo;
-      p = pp;
-    }
-  }
-  return bits;
 }
 
 template <class C>
@@ -367,7 +361,7 @@ __device__ __forceinline__ void group_sync() {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 }
 
-template <class C>
+template <class C, Role kRole>
 __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kernel(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[C::kLds];
   __shared__ int scratch[C::kThreads + 2];
@@ -391,6 +385,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
       return min(mul_div(g, total, parts_of(a, total)), total - 1);
     });
     total = uniform(w.total), parts = parts_of(a, total);
+    if (kRole == kPrefix && unit == 0 && rt == 0 && threadIdx.x == 0) *a.prefix_count = parts;
     if (g >= parts) return;
     x = uniform(mul_div(g, total, parts));
     x_end = uniform(mul_div(g + 1, total, parts));
@@ -402,7 +397,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
   const int row = rt * C::kRows + 32 * rw + (lane & 31);
   const int qrow = min(row, rows - 1), t = qrow / a.group, gh = qrow % a.group;
   const int h = lane >> 5;
-  const int64_t slot0 = ((int64_t)head * a.row_tiles + rt) * 2 * a.G;
+  const int64_t slot0 = ((int64_t)head * a.row_tiles + rt) * (2 * a.G + (kRole == kOwn ? a.batch : 0));
   const Frag<C> at(lane);
   const uint32_t ring0 = lds_addr(lds) + kw * C::S * C::kStage;
   const uint32_t pages0 = lds_addr(lds) + C::kRing + wave * (C::kAhead + 1) * C::kPages;
@@ -412,11 +407,12 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
 
   while (x < x_end) {
     const int len = a.c.len(seq);
-    const int tiles = (len + a.T + C::kTile - 1) / C::kTile;
+    const int tiles = (len + a.nodes + C::kTile - 1) / C::kTile;
     const int first = x - before, last = min(tiles, x_end - before);
     // for the join: tile y is in part floor(((y + 1) parts - 1) / total)
     if (a.pieces && first == 0 && head == 0 && rt == 0 && threadIdx.x == 0)
-      a.pieces[seq] = make_int2(g, (int)(((double)(before + tiles) * (double)parts - 1.0) / (double)total));
+      a.pieces[seq] = make_int2(
+          g, kRole == kOwn && a.whole ? g : (int)(((double)(before + tiles) * (double)parts - 1.0) / (double)total));
     const int n = last - first;  // steps
     // nothing cached: no entry of the table counts, and look-ups read the length (unused) in its place
     const int32_t* table = len > 0 ? a.c.block_table + (int64_t)seq * a.c.table_width : a.c.lens + seq;
@@ -447,12 +443,12 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
         for (int u = 0; u < C::kLoads; ++u) {
           int j = rw + C::RW * u;
           if (C::kLoadsAll % C::RW != 0) j = min(j, C::kLoadsAll - 1);  // the last rows again
-          const int row = j * C::kRowsPerLoad + rr, key = base + row;
+          const int row = j * C::kRowsPerLoad + rr, key = kRole == kPrefix ? min(base + row, len - 1) : base + row;
           const int page = min(max(wide ? wide_id : pages[row], 0), a.c.n_pages - 1);
           const int64_t cached = (int64_t)page * page_bytes +
                                  (int64_t)((head << a.c.page_shift) + (key & in_page)) * C::kRowBytes;
           const int64_t node = (((int64_t)seq * a.T + min(key - len, a.T - 1)) * Hkv + head) * C::kRowBytes;
-          const bool tree = key >= len;
+          const bool tree = kRole != kPrefix && key >= len;
           dma16<C::kOnce>((tree ? reinterpret_cast<const char*>(a.k_new) + node : kp + cached) + 16 * k_slot<C>(slot, row),
                           __builtin_amdgcn_readfirstlane(to + j * 1024));
           dma16<C::kOnce>((tree ? reinterpret_cast<const char*>(a.v_new) + node : vp + cached) + 16 * v_slot<C>(slot, row),
@@ -496,7 +492,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
 #pragma unroll
     for (int i = 0; i < C::D / 16; ++i) qf[i] = *reinterpret_cast<const bf16x8*>(a.q + qoff + 16 * i + 8 * h);
     uint64_t sees = 0, used = 0;  // of this lane's row; all used nodes
-    if (last == tiles || last * C::kTile > len) {
+    if (kRole != kPrefix && (last == tiles || last * C::kTile > len)) {
       const uint64_t bits = tree_bits(lane < a.T ? a.parents[(int64_t)seq * a.T + lane] : -2, a.T, lane);
       sees = shfl64(bits, t);
       used = __ballot(bits != 0);
@@ -534,7 +530,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
       char* kt = const_cast<char*>(ring) + i % C::S * C::kStage;
       char* vt = kt + C::kHalf;
       const int base = (first + i) * C::kTile + kw * C::kKeys;  // first key
-      const int cached = len - base, left = cached + a.T;         // of the cache's, of all, from there on
+      const int cached = len - base, left = cached + a.nodes;     // of the cache's, of all, from there on
       const bool masked = cached < C::kKeys;
       uint64_t see = ~0ull;
       if (masked) {
@@ -551,7 +547,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
         group_sync<C>();
       }
       if (left > 0) step<C>((lds_t)kt, (lds_t)vt, at, qf, a.c2, lane, masked, see, st);
-      if (masked && left > 0 && s_odd[kw]) {
+      if (kRole != kPrefix && masked && left > 0 && s_odd[kw]) {
         // what is not finite in a node's V (cleared above) reaches the rows that see the node, and no others
 #pragma unroll 1
         for (int k = max(cached, 0); k < min(C::kKeys, left); ++k) {
@@ -574,7 +570,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
     // A lane's values in fours, d = 4 h + 8 u of its row.  Key groups: joined through LDS, a
     // share of the fours to each wave (one wave for all of them: 1.8 us against 1.1 for a
     // single token).
-    const bool whole = first == 0 && last == tiles;
+    const bool whole = kRole == kTree && first == 0 && last == tiles;
     constexpr int kFours = C::D / 8, kMine = kFours / C::KW;
     float m = st.m, l = st.l + xor32(st.l, lane);
     f32x4 o[kMine];
@@ -636,11 +632,16 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
           *reinterpret_cast<uint2*>(a.out + qoff + d0 + 8 * u) = pk.u;
         }
       } else {
-        const int64_t slot = (slot0 + 2 * g + (first == 0 ? 1 : 0)) * C::kRows + 32 * rw + (lane & 31);
+        const int64_t slot = kRole == kPrefix ? ((int64_t)head * a.prefix_G + g) * rows + row
+                                              : (slot0 + (kRole == kOwn && first == 0 && last == tiles ? 2 * a.G + seq
+                                                                                                     : 2 * g + (first == 0 ? 1 : 0))) *
+                                                        C::kRows + 32 * rw + (lane & 31);
+        float* part_o = kRole == kPrefix ? a.prefix_o : a.part_o;
+        float* part_ml = kRole == kPrefix ? a.prefix_ml : a.part_ml;
 #pragma unroll
-        for (int u = 0; u < kMine; ++u) *reinterpret_cast<f32x4*>(a.part_o + slot * C::D + d0 + 8 * u) = o[u];
+        for (int u = 0; u < kMine; ++u) *reinterpret_cast<f32x4*>(part_o + slot * C::D + d0 + 8 * u) = o[u];
         if (h == 0 && kw == 0)
-          *reinterpret_cast<f32x2*>(a.part_ml + 2 * slot) = f32x2{m, last == tiles && !sees ? kUnused : l};
+          *reinterpret_cast<f32x2*>(part_ml + 2 * slot) = f32x2{m, kRole != kPrefix && last == tiles && !sees ? kUnused : l};
       }
     }
     __syncthreads();
@@ -655,7 +656,8 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
 // one go: ceil(pieces / (2 spread)) rounds of memory latency for a row.  16 rows a workgroup for few
 // pieces (spread 1), 4 for more (a wave a row), or one; by the parts for each sequence on average, so
 // a long sequence among many short ones takes more rounds than it would have to.
-template <class C>
+// kShared: a shared prefix's pieces come first.
+template <class C, bool kShared>
 __global__ __launch_bounds__(256) void tree_attention_join_kernel(AttnArgs a) {
   constexpr int kPer = C::D / 16;  // values of a lane
   constexpr int kAtOnce = 2;       // pieces in flight, per group of lanes
@@ -668,26 +670,33 @@ __global__ __launch_bounds__(256) void tree_attention_join_kernel(AttnArgs a) {
   const int row0 = blockIdx.x % chunks * each;
   const int2 at = a.pieces[seq];
   const int g0 = uniform(at.x), g1 = uniform(at.y);
-  if (g0 == g1) return;  // one piece: written already
+  const int before = kShared ? uniform(*a.prefix_count) : 0, last = before + g1 - g0;
+  if (!kShared && last == 0) return;  // one piece: written already
   const int sub = 4 * wave + (lane >> 4);  // of the workgroup's 16 groups of lanes
   const int row = row0 + sub / spread;
   const int qrow = min(row, rows - 1), t = qrow / a.group;
-  const int64_t slot0 = ((int64_t)head * a.row_tiles + qrow / C::kRows) * 2 * a.G;
-  const float end = a.part_ml[2 * ((slot0 + 2 * g1) * C::kRows + qrow % C::kRows) + 1];
+  const int64_t slot0 = ((int64_t)head * a.row_tiles + qrow / C::kRows) * (2 * a.G + (kShared ? a.batch : 0));
+  const bool whole = kShared && g0 == g1;  // a sequence in one piece
+  const float end = a.part_ml[2 * ((slot0 + (whole ? 2 * a.G + seq : 2 * g1)) * C::kRows + qrow % C::kRows) + 1];
   float m = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) o[e] = 0.f;
-  for (int g = g0 + sub % spread; g <= g1; g += kAtOnce * spread) {
+  for (int g = sub % spread; g <= last; g += kAtOnce * spread) {
     f32x2 ml[kAtOnce];
     f32x4 v[kAtOnce][kPer / 4];
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
-      const int gk = min(g + k * spread, g1);
-      const int64_t slot = (slot0 + 2 * gk + (gk == g0 ? 1 : 0)) * C::kRows + qrow % C::kRows;
-      ml[k] = *reinterpret_cast<const f32x2*>(a.part_ml + 2 * slot);
+      const int gk = min(g + k * spread, last) - before;
+      const bool shared = kShared && gk < 0;
+      const int64_t slot = shared ? ((int64_t)head * a.prefix_G + gk + before) * a.batch * rows + (int64_t)seq * rows + qrow
+                                  : (slot0 + (whole ? 2 * a.G + seq : 2 * (g0 + gk) + (gk == 0 ? 1 : 0))) * C::kRows +
+                                        qrow % C::kRows;
+      const float* part_o = shared ? a.prefix_o : a.part_o;
+      const float* part_ml = shared ? a.prefix_ml : a.part_ml;
+      ml[k] = *reinterpret_cast<const f32x2*>(part_ml + 2 * slot);
 #pragma unroll
       for (int e = 0; e < kPer / 4; ++e)
-        v[k][e] = *reinterpret_cast<const f32x4*>(a.part_o + slot * C::D + (lane & 15) * kPer + 4 * e);
+        v[k][e] = *reinterpret_cast<const f32x4*>(part_o + slot * C::D + (lane & 15) * kPer + 4 * e);
     }
     float top = m;
 #pragma unroll
@@ -699,7 +708,7 @@ __global__ __launch_bounds__(256) void tree_attention_join_kernel(AttnArgs a) {
     for (int e = 0; e < kPer; ++e) o[e] *= was;
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
-      if (g + k * spread <= g1) {
+      if (g + k * spread <= last) {
         const float f = __builtin_amdgcn_exp2f(ml[k].x - m0);
         l = fmaf(ml[k].y, f, l);
 #pragma unroll
@@ -761,12 +770,12 @@ __global__ __launch_bounds__(256) void tree_attention_join_kernel(AttnArgs a) {
   for (int e = 0; e < kPer / 4; ++e) reinterpret_cast<uint2*>(out)[e] = pk.u[e];
 }
 
-template <class C>
+template <class C, Role kRole>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
-  tree_attention_kernel<C><<<dim3((uint32_t)(cdiv((int64_t)a.G * a.c.kv_heads, 8) * 8 * a.row_tiles)), dim3(C::kThreads), 0, stream>>>(a);
+  tree_attention_kernel<C, kRole><<<dim3((uint32_t)(cdiv((int64_t)a.G * a.c.kv_heads, 8) * 8 * a.row_tiles)), dim3(C::kThreads), 0, stream>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.pieces) return e;
-  tree_attention_join_kernel<C><<<
+  tree_attention_join_kernel<C, kRole == kOwn><<<
       dim3((uint32_t)(a.batch * a.c.kv_heads * cdiv(a.T * a.group, 16 / a.spread))), dim3(256), 0, stream>>>(a);
   return hipGetLastError();
 }
@@ -799,7 +808,8 @@ AttnPlan plan_tree_attention(const CacheView& c, int64_t batch, int64_t T, int64
     p.row_tiles = cdiv(rows, C::kRows);
     // tiles when all lengths are full: no more parts than that
     const int64_t each = cdiv(((int64_t)c.table_width << c.page_shift) + T, (int64_t)C::kTile), most = batch * each;
-    p.G = 256 * C::kGroups / (p.row_tiles * c.kv_heads);
+    p.slots = 256 * C::kGroups;
+    p.G = p.slots / (p.row_tiles * c.kv_heads);
     p.G = p.G < 1 ? 1 : p.G > most ? most : p.G;
     // Few tiles a sequence at most, by the table's width (the lengths are on the device: a table for more
     // keys cuts sequences however short they are): a part for each and no join (4 x 9 nodes, page 256: 8.0 us
@@ -807,19 +817,21 @@ AttnPlan plan_tree_attention(const CacheView& c, int64_t batch, int64_t T, int64
     // against 27.9; at worst 2 x 18 nodes, 3 heads, 115 keys: 14.0 against 12.8).
     p.whole = each <= 4 || (each <= 8 && batch * c.kv_heads * p.row_tiles >= 48);
     if (p.whole) p.G = batch;
-    const int64_t slots = (int64_t)c.kv_heads * p.row_tiles * 2 * p.G * C::kRows;
+    p.tile_rows = C::kRows;
+    const int64_t rows = (int64_t)c.kv_heads * p.row_tiles * 2 * p.G * C::kRows;
     const bool join = p.G > 1 && !p.whole;
-    p.part_bytes = join ? align_up((size_t)(slots * D) * 4, 256) : 0;
-    p.ml_bytes = join ? align_up((size_t)slots * 8, 256) : 0;
+    p.part_bytes = join ? align_up((size_t)(rows * D) * 4, 256) : 0;
+    p.ml_bytes = join ? align_up((size_t)rows * 8, 256) : 0;
     p.ws_bytes = join ? p.part_bytes + p.ml_bytes + align_up((size_t)batch * 8, 256) : 0;
     return p;
   };
   return D == 64 ? with_cfg<64>(rows, plan) : with_cfg<128>(rows, plan);
 }
 
-hipError_t launch_tree_attention(const AttnPlan& p, const CacheView& c, const void* q, const void* k_new,
-                                 const void* v_new, const int32_t* parents, int64_t batch, int64_t T, int64_t group,
-                                 int64_t D, double scale, void* out, void* ws, hipStream_t stream) {
+namespace {
+
+AttnArgs attention_args(const AttnPlan& p, const CacheView& c, const void* q, const void* k_new, const void* v_new,
+                        const int32_t* parents, int64_t batch, int64_t T, int64_t group, double scale, void* out) {
   AttnArgs a{};
   a.c = c;
   a.q = static_cast<const uint16_t*>(q);
@@ -827,19 +839,87 @@ hipError_t launch_tree_attention(const AttnPlan& p, const CacheView& c, const vo
   a.v_new = static_cast<const uint16_t*>(v_new);
   a.parents = parents;
   a.out = static_cast<uint16_t*>(out);
-  a.part_o = static_cast<float*>(ws);
-  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_bytes);
-  a.pieces = p.ws_bytes == 0 ? nullptr : reinterpret_cast<int2*>(static_cast<char*>(ws) + p.part_bytes + p.ml_bytes);
   a.whole = p.whole;
   a.batch = (int)batch;
   a.T = (int)T;
+  a.nodes = (int)T;
   a.group = (int)group;
   a.G = (int)p.G;
   a.row_tiles = (int)p.row_tiles;
-  a.spread = p.G >= 32 * batch ? 16 : p.G >= 8 * batch ? 4 : 1;  // by its pieces
   a.c2 = attention_c2(scale);
-  auto run = [&](auto cfg) { return launch<decltype(cfg)>(a, stream); };
+  return a;
+}
+
+}  // namespace
+
+hipError_t launch_tree_attention(const AttnPlan& p, const CacheView& c, const void* q, const void* k_new,
+                                 const void* v_new, const int32_t* parents, int64_t batch, int64_t T, int64_t group,
+                                 int64_t D, double scale, void* out, void* ws, hipStream_t stream) {
+  AttnArgs a = attention_args(p, c, q, k_new, v_new, parents, batch, T, group, scale, out);
+  a.part_o = static_cast<float*>(ws);
+  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_bytes);
+  a.pieces = p.ws_bytes == 0 ? nullptr : reinterpret_cast<int2*>(static_cast<char*>(ws) + p.part_bytes + p.ml_bytes);
+  a.spread = p.G >= 32 * batch ? 16 : p.G >= 8 * batch ? 4 : 1;  // by its pieces
+  auto run = [&](auto cfg) { return launch<decltype(cfg), kTree>(a, stream); };
   return D == 64 ? with_cfg<64>(T * group, run) : with_cfg<128>(T * group, run);
+}
+
+SharedPlan plan_shared_attention(const CacheView& c, const CacheView& prefix, int64_t batch, int64_t T, int64_t group,
+                                 int64_t D) {
+  SharedPlan p{};
+  p.own = plan_tree_attention(c, batch, T, group, D);
+  const AttnPlan all = plan_tree_attention(prefix, 1, batch * T, group, D);
+  p.prefix_tiles = all.row_tiles;
+  const int64_t units = all.row_tiles * c.kv_heads;
+  const int64_t most = cdiv((int64_t)prefix.table_width << prefix.page_shift, 32);  // tiles have 32 keys or more
+  p.prefix_parts = std::min(most, std::max<int64_t>(1, all.slots / units));
+  const int64_t rows = c.kv_heads * p.prefix_parts * batch * T * group;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align_up(bytes, 256);
+    return at;
+  };
+  const int64_t own_rows = c.kv_heads * p.own.row_tiles * (2 * p.own.G + batch) * p.own.tile_rows;
+  p.own_o = take((size_t)(own_rows * D) * 4);
+  p.own_ml = take((size_t)own_rows * 8);
+  p.pieces = take((size_t)batch * 8);
+  p.prefix_o = take((size_t)(rows * D) * 4);
+  p.prefix_ml = take((size_t)rows * 8);
+  p.count = take(4);
+  p.ws_bytes = off;
+  return p;
+}
+
+hipError_t launch_shared_attention(const SharedPlan& p, const CacheView& c, const CacheView& prefix, const void* q,
+                                   const void* k_new, const void* v_new, const int32_t* parents, int64_t batch,
+                                   int64_t T, int64_t group, int64_t D, double scale, void* out, void* ws,
+                                   hipStream_t stream) {
+  AttnArgs a = attention_args(p.own, c, q, k_new, v_new, parents, batch, T, group, scale, out);
+  char* w = static_cast<char*>(ws);
+  a.part_o = reinterpret_cast<float*>(w + p.own_o);
+  a.part_ml = reinterpret_cast<float*>(w + p.own_ml);
+  a.pieces = reinterpret_cast<int2*>(w + p.pieces);
+  a.prefix_o = reinterpret_cast<float*>(w + p.prefix_o);
+  a.prefix_ml = reinterpret_cast<float*>(w + p.prefix_ml);
+  a.prefix_count = reinterpret_cast<int*>(w + p.count);
+  a.prefix_G = (int)p.prefix_parts;
+  const int64_t pieces = p.prefix_parts + cdiv(p.own.G, batch);
+  a.spread = pieces >= 32 ? 16 : pieces >= 8 ? 4 : 1;
+  AttnArgs b = a;
+  b.c = prefix;
+  b.batch = 1;
+  b.T = (int)(batch * T);
+  b.nodes = 0;
+  b.G = b.prefix_G;
+  b.row_tiles = (int)p.prefix_tiles;
+  b.whole = false;
+  b.pieces = nullptr;
+  auto first = [&](auto cfg) { return launch<decltype(cfg), kPrefix>(b, stream); };
+  const hipError_t e = D == 64 ? with_cfg<64>(batch * T * group, first) : with_cfg<128>(batch * T * group, first);
+  if (e != hipSuccess) return e;
+  auto then = [&](auto cfg) { return launch<decltype(cfg), kOwn>(a, stream); };
+  return D == 64 ? with_cfg<64>(T * group, then) : with_cfg<128>(T * group, then);
 }
 
 }  // namespace dfs

@@ -33,6 +33,24 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t pa = (uintptr_t)a, pb = (uintptr_t)b;
   return pa < pb + nb && pb < pa + na;
 }
+struct Span {
+  const void* p;  // NULL: nothing
+  size_t n;
+};
+// Whether one of the outputs overlaps an input or another output.  in_place[i]: the input (or -1) whose very place
+// output i may take.
+template <int NI, int NO>
+bool any_overlap(const Span (&in)[NI], const Span (&out)[NO], const int (&in_place)[NO]) {
+  for (int i = 0; i < NO; ++i) {
+    if (!out[i].p) continue;
+    for (int j = 0; j < NI; ++j)
+      if (in[j].p && overlaps(out[i].p, out[i].n, in[j].p, in[j].n) && !(in_place[i] == j && out[i].p == in[j].p))
+        return true;
+    for (int j = 0; j < i; ++j)
+      if (out[j].p && overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+  }
+  return false;
+}
 int esize(dfs_dtype_t t) { return t == DFS_BF16 ? 2 : 4; }
 bool valid_dtype(int t) { return t == DFS_F32 || t == DFS_BF16; }
 
@@ -742,6 +760,216 @@ int dfs_cache_commit(const void* k_new, const void* v_new, const int32_t* nodes,
   (void)hipGetLastError();
   return hip_status(launch_cache_commit(cache_view(s, k_pages, v_pages, block_table, lens), k_new, v_new, nodes,
                                         counts, s.batch, s.T, path_len, out_lens, stream));
+}
+
+int dfs_tree_positions(const int32_t* parents, const int32_t* lens, const int32_t* prefix_len, int64_t batch,
+                       int64_t T, int32_t* out, hipStream_t stream) {
+  if (!parents || !lens || !out) return DFS_E_NULL;
+  if (batch < 1 || batch > 65536 || T < 1 || T > DFS_MAX_NODES) return DFS_E_SHAPE;
+  if (!aligned(parents, 4) || !aligned(lens, 4) || !aligned(prefix_len, 4) || !aligned(out, 4)) return DFS_E_ALIGN;
+  const size_t n = (size_t)(batch * T) * 4;
+  const Span in[3] = {{parents, n}, {lens, (size_t)batch * 4}, {prefix_len, 4}}, outs[1] = {{out, n}};
+  if (any_overlap(in, outs, {-1})) return DFS_E_ARG;
+  int st = check_device();
+  if (st != DFS_OK) return st;
+  (void)hipGetLastError();
+  return hip_status(launch_tree_positions(parents, lens, prefix_len, batch, T, out, stream));
+}
+
+int dfs_rope_frequencies(int64_t rot_dim, double base, dfs_rope_scaling_t scaling, double factor, double original,
+                         double beta_fast, double beta_slow, float* out_freqs, double* out_amplitude) {
+  if (!out_freqs) return DFS_E_NULL;
+  if (rot_dim < 2 || rot_dim > 1024) return DFS_E_SHAPE;
+  if (rot_dim % 2 != 0 || scaling < DFS_ROPE_PLAIN || scaling > DFS_ROPE_BANDS) return DFS_E_UNSUPPORTED;
+  if (!(std::isfinite(base) && base > 1.0)) return DFS_E_ARG;
+  if (scaling != DFS_ROPE_PLAIN && !(std::isfinite(factor) && factor >= 1.0)) return DFS_E_ARG;
+  if (scaling == DFS_ROPE_NTK && rot_dim < 4) return DFS_E_ARG;
+  const bool betas = scaling == DFS_ROPE_YARN || scaling == DFS_ROPE_BANDS;
+  if (betas && !(std::isfinite(original) && original >= 1.0 && beta_slow > 0.0 && beta_fast > beta_slow &&
+                 std::isfinite(beta_fast)))
+    return DFS_E_ARG;
+  constexpr double kTurn = 6.283185307179586476925;  // 2 pi
+  const double n = (double)rot_dim;
+  const double b = scaling == DFS_ROPE_NTK ? base * std::pow(factor, n / (n - 2.0)) : base;
+  double low = 0.0, high = 1.0;
+  if (scaling == DFS_ROPE_YARN) {
+    // the pair whose angle turns `beta` times over the original positions
+    auto pair_of = [&](double beta) { return n * std::log(original / (kTurn * beta)) / (2.0 * std::log(base)); };
+    low = std::fmin(std::fmax(std::floor(pair_of(beta_fast)), 0.0), n - 1.0);
+    high = std::fmin(std::fmax(std::ceil(pair_of(beta_slow)), 0.0), n - 1.0);
+    if (high <= low) high = low + 1e-3;  // a step
+  }
+  for (int64_t i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(b, -2.0 * (double)i / n);
+    if (scaling == DFS_ROPE_LINEAR) {
+      f /= factor;
+    } else if (scaling == DFS_ROPE_YARN) {
+      const double r = std::fmin(std::fmax(((double)i - low) / (high - low), 0.0), 1.0);
+      f = f * (1.0 - r) + f / factor * r;
+    } else if (scaling == DFS_ROPE_BANDS) {
+      const double turns = original * f / kTurn;  // over the original positions
+      const double r = std::fmin(std::fmax((turns - beta_slow) / (beta_fast - beta_slow), 0.0), 1.0);
+      f = (1.0 - r) * f / factor + r * f;
+    }
+    out_freqs[i] = (float)f;
+  }
+  if (out_amplitude) *out_amplitude = scaling == DFS_ROPE_YARN && factor > 1.0 ? 0.1 * std::log(factor) + 1.0 : 1.0;
+  return DFS_OK;
+}
+
+// What rope's sizes must be with these of q, k and v given.
+static int check_rope_shape(const dfs_rope_shape_t* s, bool q, bool k, bool v, int64_t least_rot) {
+  if (!s) return DFS_E_NULL;
+  if (!valid_dtype(s->dtype) || (s->layout != DFS_ROPE_HALF && s->layout != DFS_ROPE_INTERLEAVED))
+    return DFS_E_UNSUPPORTED;
+  if (s->rows < 1 || s->rows > DFS_MAX_ROWS || s->head_dim < 8 || s->head_dim > 1024 || s->rot_dim < least_rot ||
+      s->rot_dim > s->head_dim || (q && (s->q_heads < 1 || s->q_heads > 1024)) ||
+      ((k || v) && (s->kv_heads < 1 || s->kv_heads > 1024)))
+    return DFS_E_SHAPE;
+  if (s->head_dim % 8 != 0 || s->rot_dim % 2 != 0) return DFS_E_UNSUPPORTED;
+  const struct {
+    bool there;
+    int64_t stride, heads;
+  } of[3] = {{q, s->q_stride, s->q_heads}, {k, s->k_stride, s->kv_heads}, {v, s->v_stride, s->kv_heads}};
+  for (const auto& x : of) {
+    if (!x.there) continue;
+    if (x.stride < x.heads * s->head_dim || x.stride > ((int64_t)1 << 31)) return DFS_E_SHAPE;
+    if (x.stride % 8 != 0) return DFS_E_UNSUPPORTED;
+  }
+  const float amplitude = (float)s->amplitude;
+  if (!(std::isfinite(amplitude) && amplitude > 0.f)) return DFS_E_ARG;
+  return DFS_OK;
+}
+
+// The bytes that an input of `heads` heads spans, and that its dense rows have.
+static Span strided(const void* p, const dfs_rope_shape_t& s, int64_t stride, int64_t heads) {
+  return {p, (size_t)((s.rows - 1) * stride + heads * s.head_dim) * esize(s.dtype)};
+}
+static Span dense(const void* p, const dfs_rope_shape_t& s, int64_t heads) {
+  return {p, (size_t)(s.rows * heads * s.head_dim) * esize(s.dtype)};
+}
+
+static RopeJob rope_job(const dfs_rope_shape_t& s, const void* q, const void* k, const void* v, const float* freqs,
+                        void* out_q, void* out_k, void* out_v) {
+  return RopeJob{{{q, out_q, s.q_stride, q ? (int)s.q_heads : 0},
+                  {k, out_k, s.k_stride, k ? (int)s.kv_heads : 0},
+                  {v, out_v, s.v_stride, v ? (int)s.kv_heads : 0}},
+                 freqs,
+                 s.rows,
+                 (int)s.head_dim,
+                 (int)s.rot_dim,
+                 (float)s.amplitude,
+                 s.layout == DFS_ROPE_INTERLEAVED,
+                 s.dtype == DFS_BF16};
+}
+
+int dfs_rope(const void* q, const void* k, const void* v, const int32_t* positions, const float* freqs,
+             const dfs_rope_shape_t* shape, void* out_q, void* out_k, void* out_v, hipStream_t stream) {
+  if ((!q && !k) || !positions || !freqs || !q != !out_q || !k != !out_k || !v != !out_v) return DFS_E_NULL;
+  int st = check_rope_shape(shape, q, k, v, 2);
+  if (st != DFS_OK) return st;
+  const dfs_rope_shape_t s = *shape;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out_q, 16) || !aligned(out_k, 16) ||
+      !aligned(out_v, 16) || !aligned(positions, 4) || !aligned(freqs, 4))
+    return DFS_E_ALIGN;
+  const Span in[5] = {strided(q, s, s.q_stride, s.q_heads), strided(k, s, s.k_stride, s.kv_heads),
+                      strided(v, s, s.v_stride, s.kv_heads), {positions, (size_t)s.rows * 4},
+                      {freqs, (size_t)s.rot_dim * 2}};
+  const Span out[3] = {dense(out_q, s, s.q_heads), dense(out_k, s, s.kv_heads), dense(out_v, s, s.kv_heads)};
+  const int place[3] = {s.q_stride == s.q_heads * s.head_dim ? 0 : -1, s.k_stride == s.kv_heads * s.head_dim ? 1 : -1, -1};
+  if (any_overlap(in, out, place)) return DFS_E_ARG;
+  if ((st = check_device()) != DFS_OK) return st;
+  (void)hipGetLastError();
+  return hip_status(launch_rope(rope_job(s, q, k, v, freqs, out_q, out_k, out_v), positions, stream));
+}
+
+int dfs_cache_append(const void* q, const void* k, const void* v, const int32_t* starts, const float* freqs,
+                     const dfs_rope_shape_t* rope, const int32_t* prefix_len, void* out_q, void* k_pages,
+                     void* v_pages, const int32_t* block_table, const int32_t* lens, const dfs_cache_shape_t* shape,
+                     int32_t* out_lens, hipStream_t stream) {
+  if (!k || !v || !starts || !k_pages || !v_pages || !block_table || !lens || !q != !out_q) return DFS_E_NULL;
+  int st = check_rope_shape(rope, q, true, true, 0);
+  if (st != DFS_OK) return st;
+  const dfs_rope_shape_t r = *rope;
+  if (r.rot_dim > 0 && !freqs) return DFS_E_NULL;
+  if (!shape) return DFS_E_NULL;
+  dfs_cache_shape_t s = *shape;
+  s.T = 1;  // not looked at
+  if ((st = check_cache_shape(&s)) != DFS_OK) return st;
+  if (s.kv_heads != r.kv_heads || s.head_dim != r.head_dim || s.dtype != r.dtype) return DFS_E_SHAPE;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out_q, 16) || !aligned(k_pages, 16) ||
+      !aligned(v_pages, 16) || !aligned(starts, 4) || !aligned(freqs, 4) || !aligned(prefix_len, 4) ||
+      !aligned(block_table, 4) || !aligned(lens, 4) || !aligned(out_lens, 4))
+    return DFS_E_ALIGN;
+  const size_t pn = pool_bytes(s), bn = (size_t)s.batch * 4;
+  const Span in[8] = {strided(q, r, r.q_stride, r.q_heads), strided(k, r, r.k_stride, r.kv_heads),
+                      strided(v, r, r.v_stride, r.kv_heads), {starts, bn + 4},
+                      {r.rot_dim > 0 ? freqs : nullptr, (size_t)r.rot_dim * 2}, {prefix_len, 4},
+                      {block_table, (size_t)(s.batch * s.table_width) * 4}, {lens, bn}};
+  const Span out[4] = {dense(out_q, r, r.q_heads), {k_pages, pn}, {v_pages, pn}, {out_lens, bn}};
+  if (any_overlap(in, out, {r.q_stride == r.q_heads * r.head_dim ? 0 : -1, -1, -1, -1})) return DFS_E_ARG;
+  if ((st = check_device()) != DFS_OK) return st;
+  (void)hipGetLastError();
+  return hip_status(launch_cache_append(rope_job(r, q, k, v, freqs, out_q, nullptr, nullptr),
+                                        cache_view(s, k_pages, v_pages, block_table, lens), starts, prefix_len, s.batch,
+                                        out_lens, stream));
+}
+
+// The prefix as the one sequence of a table of its own.
+static CacheView prefix_view(const dfs_cache_shape_t& s, const void* k_pages, const void* v_pages,
+                             const int32_t* prefix_table, const int32_t* prefix_len, int64_t prefix_width) {
+  dfs_cache_shape_t one = s;
+  one.table_width = prefix_width;
+  return cache_view(one, k_pages, v_pages, prefix_table, prefix_len);
+}
+
+static int check_shared_shape(const dfs_cache_shape_t* s, int64_t prefix_width) {
+  const int st = check_attention_shape(s);
+  if (st != DFS_OK) return st;
+  return prefix_width < 1 || prefix_width > ((int64_t)1 << 30) / s->page_size ? DFS_E_SHAPE : DFS_OK;
+}
+
+size_t dfs_tree_attention_shared_workspace_bytes(const dfs_cache_shape_t* shape, int64_t prefix_width) {
+  if (check_shared_shape(shape, prefix_width) != DFS_OK) return 0;
+  return plan_shared_attention(cache_view(*shape, nullptr, nullptr, nullptr, nullptr),
+                               prefix_view(*shape, nullptr, nullptr, nullptr, nullptr, prefix_width), shape->batch,
+                               shape->T, shape->q_heads / shape->kv_heads, shape->head_dim)
+      .ws_bytes;
+}
+
+int dfs_tree_attention_shared(const void* q, const void* k_new, const void* v_new, const int32_t* parents,
+                              const void* k_pages, const void* v_pages, const int32_t* prefix_table,
+                              const int32_t* prefix_len, int64_t prefix_width, const int32_t* block_table,
+                              const int32_t* lens, const dfs_cache_shape_t* shape, double scale, void* out, void* ws,
+                              size_t ws_bytes, hipStream_t stream) {
+  if (!q || !k_new || !v_new || !parents || !k_pages || !v_pages || !prefix_table || !prefix_len || !block_table ||
+      !lens || !out)
+    return DFS_E_NULL;
+  int st = check_shared_shape(shape, prefix_width);
+  if (st != DFS_OK) return st;
+  const dfs_cache_shape_t s = *shape;
+  if (!aligned(q, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_pages, 16) ||
+      !aligned(v_pages, 16) || !aligned(out, 16) || !aligned(parents, 4) || !aligned(block_table, 4) ||
+      !aligned(lens, 4) || !aligned(prefix_table, 4) || !aligned(prefix_len, 4))
+    return DFS_E_ALIGN;
+  const float c2 = attention_c2(scale);
+  if (!(std::isfinite(c2) && c2 > 0.f)) return DFS_E_ARG;
+  const size_t qn = (size_t)(s.batch * s.T * s.q_heads * s.head_dim) * 2, nn = nodes_bytes(s), pn = pool_bytes(s);
+  const Span in[10] = {{q, qn}, {k_new, nn}, {v_new, nn}, {parents, (size_t)(s.batch * s.T) * 4}, {k_pages, pn},
+                       {v_pages, pn}, {prefix_table, (size_t)prefix_width * 4}, {prefix_len, 4},
+                       {block_table, (size_t)(s.batch * s.table_width) * 4}, {lens, (size_t)s.batch * 4}};
+  const Span outs[1] = {{out, qn}};
+  if (any_overlap(in, outs, {-1})) return DFS_E_ARG;
+  const int64_t group = s.q_heads / s.kv_heads;
+  const CacheView c = cache_view(s, k_pages, v_pages, block_table, lens);
+  const CacheView prefix = prefix_view(s, k_pages, v_pages, prefix_table, prefix_len, prefix_width);
+  const SharedPlan p = plan_shared_attention(c, prefix, s.batch, s.T, group, s.head_dim);
+  if (!ws || ws_bytes < p.ws_bytes) return DFS_E_WORKSPACE;
+  if (!aligned(ws, 256)) return DFS_E_ALIGN;
+  if ((st = check_device()) != DFS_OK) return st;
+  (void)hipGetLastError();
+  return hip_status(launch_shared_attention(p, c, prefix, q, k_new, v_new, parents, s.batch, s.T, group, s.head_dim,
+                                            scale, out, ws, stream));
 }
 
 }  // extern "C"

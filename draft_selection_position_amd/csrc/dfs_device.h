@@ -141,6 +141,25 @@ __device__ __forceinline__ int lanes_below(uint64_t mask) {
                                         __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
 }
 
+// The nodes that node `lane` (parent p; none: -2) sees, as bits (none for an unused node):
+// itself and, by doubling along the parents, its ancestors.
+__device__ __forceinline__ uint64_t tree_bits(int p, int T, int lane) {
+  const bool used = p >= -1 && p < lane;
+  uint64_t bits = used ? 1ull << lane : 0;
+  if (!used) p = -1;
+#pragma unroll 1
+  for (int reach = 1; reach < T; reach *= 2) {
+    const int src = p < 0 ? lane : p;
+    const uint32_t lo = __shfl((uint32_t)bits, src), hi = __shfl((uint32_t)(bits >> 32), src);
+    const int pp = __shfl(p, src);
+    if (p >= 0) {
+      bits |= ((uint64_t)hi << 32) | lo;
+      p = pp;
+    }
+  }
+  return bits;
+}
+
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ float uniformf(float x) {
   return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));

@@ -220,9 +220,33 @@ hipError_t launch_cache_commit(const CacheView& c, const void* k_new, const void
                                const int32_t* counts, int64_t batch, int64_t T, int64_t P, int32_t* out_lens,
                                hipStream_t stream);
 
+// ---------------------------------------------------------------- rotary positions
+hipError_t launch_tree_positions(const int32_t* parents, const int32_t* lens, const int32_t* prefix_len, int64_t batch,
+                                 int64_t T, int32_t* out, hipStream_t stream);
+// Heads of queries, keys and values (kinds 0, 1, 2) on their way from a token's rows to dense rows or pages.
+struct RopeHeads {
+  const void* in;  // NULL: none
+  void* out;       // of keys and values in the cache: unused
+  int64_t stride;  // values from a token to the next
+  int heads;
+};
+struct RopeJob {
+  RopeHeads of[3];
+  const float* freqs;
+  int64_t rows;
+  int head_dim, rot_dim;
+  float amplitude;
+  bool interleaved, bf16;
+};
+hipError_t launch_rope(const RopeJob& job, const int32_t* positions, hipStream_t stream);
+hipError_t launch_cache_append(const RopeJob& job, const CacheView& c, const int32_t* starts, const int32_t* prefix_len,
+                               int64_t batch, int32_t* out_lens, hipStream_t stream);
+
 struct AttnPlan {
   int64_t row_tiles;       // workgroups for a head's rows
   int64_t G;               // parts that the keys of a head are cut into
+  int64_t slots;           // workgroups that the card holds at once
+  int64_t tile_rows;       // of a row tile
   bool whole;              // parts are sequences: nothing to join
   size_t part_bytes;       // of the parts' fp32 sums,
   size_t ml_bytes;         // of their maxima and sums; each sequence's parts follow
@@ -234,5 +258,20 @@ AttnPlan plan_tree_attention(const CacheView& c, int64_t batch, int64_t T, int64
 hipError_t launch_tree_attention(const AttnPlan& p, const CacheView& c, const void* q, const void* k_new,
                                  const void* v_new, const int32_t* parents, int64_t batch, int64_t T, int64_t group,
                                  int64_t D, double scale, void* out, void* ws, hipStream_t stream);
+
+// The same over a prefix that the batch shares, `prefix` being its one-sequence cache.
+struct SharedPlan {
+  AttnPlan own;            // of the sequences' own keys
+  int64_t prefix_parts;    // that the prefix is cut into, at most
+  int64_t prefix_tiles;    // row tiles of the whole batch's rows
+  size_t own_o, own_ml, pieces, prefix_o, prefix_ml, count;  // offsets in the workspace
+  size_t ws_bytes;
+};
+SharedPlan plan_shared_attention(const CacheView& c, const CacheView& prefix, int64_t batch, int64_t T, int64_t group,
+                                 int64_t D);
+hipError_t launch_shared_attention(const SharedPlan& p, const CacheView& c, const CacheView& prefix, const void* q,
+                                   const void* k_new, const void* v_new, const int32_t* parents, int64_t batch,
+                                   int64_t T, int64_t group, int64_t D, double scale, void* out, void* ws,
+                                   hipStream_t stream);
 
 }  // namespace dfs

@@ -19,7 +19,8 @@
  *
  * Conventions shared by every entry point
  *   - Every pointer argument is DEVICE memory owned by the caller, except the
- *     dfs_shape_t pointer, which is host memory read during the call only.  The
+ *     shape structs, which are host memory read during the call only (and
+ *     dfs_rope_frequencies, which runs on the host).  The
  *     library allocates no memory and keeps no pointer after it returns.
  *   - Every call only enqueues kernels on `stream` (NULL = the device's null
  *     stream) on the current HIP device and returns without synchronising.
@@ -431,6 +432,114 @@ int dfs_tree_attention(const void* q, const void* k_new, const void* v_new, cons
 int dfs_cache_commit(const void* k_new, const void* v_new, const int32_t* nodes, const int32_t* counts,
                      int64_t path_len, void* k_pages, void* v_pages, const int32_t* block_table,
                      const int32_t* lens, const dfs_cache_shape_t* shape, int32_t* out_lens, hipStream_t stream);
+
+/* ---------------------------------------------------------------- positions of a tree's nodes
+ * The position that a drafted node's rotation (dfs_rope) takes: the number of tokens before it,
+ * which are the shared prefix's, the sequence's cached ones and the node's ancestors:
+ *   out[b, t] = prefix_len + lens[b] + (number of t's ancestors)
+ * parents [batch, T] int32 as for dfs_tree_attention (an unused node counts as nobody's ancestor,
+ * and its own position is that of a node without ancestors); lens [batch] int32; prefix_len [1]
+ * int32 or NULL (0).  Both are clamped to [0, 2^30] and the result to 2^31 - 1.  out [batch, T]
+ * int32, overlapping no input.  1 <= batch <= 65536, 1 <= T <= DFS_MAX_NODES.  Alignment: 4 bytes. */
+int dfs_tree_positions(const int32_t* parents, const int32_t* lens, const int32_t* prefix_len, int64_t batch,
+                       int64_t T, int32_t* out, hipStream_t stream);
+
+/* ---------------------------------------------------------------- rotary positions
+ * The first rot_dim values of each head in pairs, each pair turned by an angle that grows with
+ * the token's position:
+ *   (x1, x2) -> A (x1 cos a - x2 sin a,  x2 cos a + x1 sin a),   a = position freqs[i]
+ *   DFS_ROPE_HALF: pair i is (x[i], x[i + rot_dim / 2]); DFS_ROPE_INTERLEAVED: (x[2 i], x[2 i + 1])
+ * The rest of a head is copied (A does not apply to it).  The angle's product and its reduction
+ * are taken in 64 bits, so that far positions lose nothing; sine, cosine and the turn in fp32,
+ * rounded once. */
+typedef enum DFS_ENUM_BASE { DFS_ROPE_HALF = 0, DFS_ROPE_INTERLEAVED = 1 } dfs_rope_layout_t;
+typedef struct {
+  int64_t rows;      /* tokens, 1..DFS_MAX_ROWS */
+  int64_t q_heads;   /* 1..1024 (not looked at without q) */
+  int64_t kv_heads;  /* 1..1024 (not looked at without k and v) */
+  int64_t head_dim;  /* a multiple of 8 in [8, 1024] */
+  int64_t rot_dim;   /* even, in [2, head_dim]; dfs_cache_append also takes 0: nothing is turned */
+  int64_t q_stride;  /* values from one token's heads to the next one's in the input: a multiple of 8, at least */
+  int64_t k_stride;  /* heads * head_dim and at most 2^31: the three may be slices of a joint projection's rows */
+  int64_t v_stride;
+  double amplitude;  /* A: > 0, neither zero nor infinite in fp32 */
+  dfs_rope_layout_t layout;
+  dfs_dtype_t dtype; /* of q, k, v and the outputs */
+} dfs_rope_shape_t;
+
+/* The frequencies freqs[i], i < rot_dim / 2, of a model's configuration, and the amplitude A that goes with
+ * them.  HOST memory on both sides, computed in 64 bits; a program does this once.  With f_i = base^(-2 i / rot_dim):
+ *   DFS_ROPE_PLAIN   f_i
+ *   DFS_ROPE_LINEAR  f_i / factor  (positions interpolated)
+ *   DFS_ROPE_NTK     f_i with base factor^(rot_dim / (rot_dim - 2)) in base's place (rot_dim >= 4)
+ *   DFS_ROPE_YARN    f_i (1 - r) + f_i / factor r  with r rising from 0 to 1 between the pairs that turn beta_fast
+ *                    and beta_slow times over `original` positions (the pairs' numbers
+ *                    rot_dim ln(original / (2 pi beta)) / (2 ln base), the lower rounded down, the upper up, within
+ *                    [0, rot_dim - 1]), and A = 0.1 ln(factor) + 1 for factor > 1  (Peng et al., "YaRN: Efficient
+ *                    Context Window Extension of Large Language Models", 2023)
+ *   DFS_ROPE_BANDS   f_i for wavelengths 2 pi / f_i below original / beta_fast, f_i / factor above
+ *                    original / beta_slow, and between them (1 - r) f_i / factor + r f_i with
+ *                    r = (original f_i / (2 pi) - beta_slow) / (beta_fast - beta_slow)
+ * base > 1, factor >= 1, original >= 1 and beta_fast > beta_slow > 0 where the schedule takes them, all finite.
+ * out_amplitude may be NULL. */
+typedef enum DFS_ENUM_BASE {
+  DFS_ROPE_PLAIN = 0,
+  DFS_ROPE_LINEAR = 1,
+  DFS_ROPE_NTK = 2,
+  DFS_ROPE_YARN = 3,
+  DFS_ROPE_BANDS = 4
+} dfs_rope_scaling_t;
+int dfs_rope_frequencies(int64_t rot_dim, double base, dfs_rope_scaling_t scaling, double factor, double original,
+                         double beta_fast, double beta_slow, float* out_freqs, double* out_amplitude);
+
+/* Queries and keys turned, values copied: the heads of a joint projection's rows, split into the
+ * dense arrays that dfs_tree_attention and dfs_cache_commit take.
+ *   q, k, v [rows, heads, head_dim] with their strides, any of them NULL together with its output
+ *   (at least one of q and k is there); positions [rows] int32 (any value); freqs [rot_dim / 2] fp32
+ *   out_q, out_k, out_v [rows, heads, head_dim] dense.  out_q may be q itself and out_k k where the
+ *   stride is heads * head_dim; otherwise an output overlaps no input and no other output.
+ * What is not finite in a value reaches its own pair (and nothing else).
+ * Alignment: positions, freqs 4 bytes, the others 16. */
+int dfs_rope(const void* q, const void* k, const void* v, const int32_t* positions, const float* freqs,
+             const dfs_rope_shape_t* shape, void* out_q, void* out_k, void* out_v, hipStream_t stream);
+
+/* ---------------------------------------------------------------- append to the cache
+ * Tokens of several sequences, one after the other, into a paged cache, their keys turned on the
+ * way (and, if given, their queries): rows starts[b] .. starts[b + 1] - 1 are the tokens behind
+ * sequence b's lens[b] cached ones.  Row starts[b] + i goes to the sequence's position lens[b] + i,
+ * and is turned by the angles of position prefix_len + lens[b] + i.
+ *   q (NULL: none), k, v and out_q as for dfs_rope (rope->rot_dim 0: keys and queries as they are,
+ *   freqs not looked at); starts [batch + 1] int32, not decreasing, within [0, rows]; prefix_len [1]
+ *   int32 or NULL (0); pools, block_table, lens (negative: 0) and shape as for dfs_cache_commit, with
+ *   shape's T and q_heads not looked at and its kv_heads, head_dim and dtype those of `rope`;
+ *   out_lens [batch] int32 (or NULL) = lens[b] + starts[b + 1] - starts[b], another buffer than lens.
+ * The pages that are written must be the sequence's own.  A token whose position lies past the table
+ * or whose page is not one of the pool's is not written (its query is turned all the same); rows
+ * before starts[0] and from starts[batch] on are no tokens: nothing is written for them, nor to
+ * their rows of out_q.
+ * Alignment: the int32 arrays and freqs 4 bytes, the others 16. */
+int dfs_cache_append(const void* q, const void* k, const void* v, const int32_t* starts, const float* freqs,
+                     const dfs_rope_shape_t* rope, const int32_t* prefix_len, void* out_q, void* k_pages,
+                     void* v_pages, const int32_t* block_table, const int32_t* lens, const dfs_cache_shape_t* shape,
+                     int32_t* out_lens, hipStream_t stream);
+
+/* ---------------------------------------------------------------- tree attention over a shared prefix
+ * dfs_tree_attention for a batch whose sequences all begin with the same prefix (a system prompt,
+ * a document, one prompt's many answers) that lies in the pool once: node t of sequence b sees the
+ * prefix's positions 0 .. prefix_len - 1, its sequence's own cache, itself and its ancestors, under one
+ * softmax.  The prefix's keys and values meet the query rows of the whole batch in one matrix
+ * product: they are read once for all sequences (for every 128 or 256 query rows of a kv head).
+ *   prefix_table [prefix_width] int32: the prefix's pages, prefix_len [1] int32 (clamped to
+ *   [0, prefix_width * page_size]; entries past it are not read, those that are, clamped to the pool);
+ *   everything else as for dfs_tree_attention (lens and block_table are of what follows the prefix).
+ * 1 <= prefix_width, prefix_width * page_size <= 2^30; out does not overlap the prefix's arrays either.
+ * ws: dfs_tree_attention_shared_workspace_bytes(shape, prefix_width) bytes of scratch (never 0). */
+size_t dfs_tree_attention_shared_workspace_bytes(const dfs_cache_shape_t* shape, int64_t prefix_width);
+int dfs_tree_attention_shared(const void* q, const void* k_new, const void* v_new, const int32_t* parents,
+                              const void* k_pages, const void* v_pages, const int32_t* prefix_table,
+                              const int32_t* prefix_len, int64_t prefix_width, const int32_t* block_table,
+                              const int32_t* lens, const dfs_cache_shape_t* shape, double scale, void* out, void* ws,
+                              size_t ws_bytes, hipStream_t stream);
 
 /* Static, NUL-terminated description of a status code; never NULL. */
 const char* dfs_status_str(int status);
