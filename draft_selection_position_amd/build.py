@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdfs.so")
 SOURCES = ["topk.hip", "gate.hip", "select.hip", "verify.hip", "conv.hip", "lmhead.hip", "static_scratch.hip",
-           "norm.hip", "linear.hip", "attention.hip", "cache.hip", "rope.hip", "dfs_api.cpp"]
+           "norm.hip", "linear.hip", "attention.hip", "prefix.hip", "cache.hip", "rope.hip", "dfs_api.cpp"]
 ARCH = "gfx950"
 
 # -packed-fp32-ops: keep the compiler from emitting packed fp32 VALU ops.
@@ -33,7 +33,7 @@ COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-Wno-unused-result",
 # them back and forth (attention of one token: 12.1 us against 11.8; the 8-bit product in
 # 128 x 128 tiles, 1024 x 10240 x 5120: 88 against 84).
 _SUMS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
-SOURCE_FLAGS = {"attention.hip": _SUMS, "linear.hip": _SUMS}
+SOURCE_FLAGS = {"attention.hip": _SUMS, "prefix.hip": _SUMS, "linear.hip": _SUMS}
 
 
 def hipcc() -> str:

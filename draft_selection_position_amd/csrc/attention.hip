@@ -31,22 +31,13 @@
 // memory latencies (lengths, pages, keys, pieces); its 16 MB would take 2.5.
 #include <algorithm>
 
-#include "dfs_device.h"
+#include "attn_tile.h"
 #include "dfs_internal.h"
-#include "mfma_big.h"
 
 namespace dfs {
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
 constexpr float kUnused = -1.0f;  // for a sum of weights
-constexpr float kLag = 8.0f;  // a maximum may lag this far (in powers of two) before sums are rescaled
 
 // What a workgroup's keys are: a sequence's cache and tree, the whole answer; the same of a batch with a shared
 // prefix, whose part of the answer is still to be joined with the prefix's; or the prefix, for the rows of the whole
@@ -63,9 +54,14 @@ struct AttnArgs {
   float* part_o;   // [Hkv, row tiles, 2 G, rows of a tile, D]; kOwn: 2 G + batch, the last for sequences in one piece
   float* part_ml;  // [Hkv, row tiles, 2 G, rows of a tile, 2]: maximum and sum; of an unused node's row the last piece has kUnused
   int2* pieces;    // [batch]: the first and the last part with a tile of the sequence (NULL: nothing to join)
-  // the shared prefix's pieces: [Hkv, parts, rows of the batch, D] and their maxima and sums, and how many there are
+  // a shared prefix's pieces: [Hkv, slots, rows of a tile, D] as the prefix's own kernel leaves them, or by tree
+  // attention's [Hkv, parts, rows of the batch, D] with their count, and their maxima and sums
   float* prefix_o;
   float* prefix_ml;
+  bool large;
+  PrefixCut cut;
+  const int32_t* prefix_len;
+  int prefix_most;  // the longest that its table has
   int* prefix_count;
   int prefix_G;
   int batch, T, group, G, row_tiles;
@@ -109,46 +105,6 @@ struct Cfg {
   static constexpr bool kEven = kGroups * kWaves > 8;
   static constexpr int kMinWaves = kGroups * kWaves > 8 ? 3 : kGroups * kWaves > 4 ? 2 : 1;  // per SIMD
 };
-
-// 16 bytes per lane from memory straight into LDS at lds_base + 16 lane; kOnce: nobody else
-// reads them (64 sequences x 17 nodes, 8192 keys: 203 us against 221 without the hint).
-template <bool kOnce>
-__device__ __forceinline__ void dma16(const void* p, uint32_t lds_base) {
-  if constexpr (kOnce)
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt"
-                 :
-                 : "v"(p), "s"(lds_base)
-                 : "memory", "m0");
-  else
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
-                 :
-                 : "v"(p), "s"(lds_base)
-                 : "memory", "m0");
-}
-
-// 4 bytes per lane, at lds_base + 4 lane.
-__device__ __forceinline__ void dma4(const void* p, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(p), "s"(lds_base) : "memory", "m0");
-}
-
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return (uint32_t)reinterpret_cast<uintptr_t>((big::lds_ptr_t)p);
-}
-
-// Where chunk c of key `row` lies: K so that 16 rows' equal chunks, V so that four rows'
-// equal 64-byte blocks fall on distinct banks.
-template <class C>
-__device__ __forceinline__ int k_slot(int c, int row) {
-  return C::kChunks == 16 ? c ^ (row & 15) : c ^ ((row >> 1) & 7);
-}
-template <class C>
-__device__ __forceinline__ int v_slot(int c, int row) {
-  return C::kChunks == 16 ? c ^ ((row & 3) << 2) : c ^ (((row >> 1) & 1) << 2);
-}
-
-__device__ __forceinline__ float xor32(float x, int lane) {
-  return __uint_as_float(xor_lanes(__float_as_uint(x), 32, lane));
-}
 
 __device__ __forceinline__ uint64_t shfl64(uint64_t x, int src) {
   return ((uint64_t)(uint32_t)__shfl((uint32_t)(x >> 32), src) << 32) | (uint32_t)__shfl((uint32_t)x, src);
@@ -255,23 +211,6 @@ __device__ __forceinline__ bool clear_rows(char* vt, int rw, int lane, uint64_t 
   }
   return odd;
 }
-
-typedef __attribute__((address_space(3))) char* lds_t;
-
-// Where a lane's fragments of a tile lie, from the start of its K (or V) rows.  K: key
-// `lane % 32`, chunk 2 x + half at k ^ 32 x.  V: keys 4 half + lane / 4 % 4 (+ 8, 16, ...),
-// the 16 d of the lane's group of 16 in 64-byte block dt at v[dt].
-template <class C>
-struct Frag {
-  uint32_t k, v[C::D / 32];
-  __device__ __forceinline__ explicit Frag(int lane) {
-    const int r = lane & 31, h = lane >> 5, q = (lane >> 2) & 3;
-    k = r * C::kRowBytes + 16 * k_slot<C>(h, r);
-#pragma unroll
-    for (int dt = 0; dt < C::D / 32; ++dt)
-      v[dt] = (4 * h + q) * C::kRowBytes + 16 * v_slot<C>(4 * dt + 2 * ((lane >> 4) & 1), q) + 8 * (lane & 3);
-  }
-};
 
 // A step's keys: scores, weights, sums.  `masked`: only the keys whose bit is set in this
 // lane's `sees` count.  Its tiles of 32 keys go side by side, so that one's matrix products
@@ -670,11 +609,28 @@ __global__ __launch_bounds__(256) void tree_attention_join_kernel(AttnArgs a) {
   const int row0 = blockIdx.x % chunks * each;
   const int2 at = a.pieces[seq];
   const int g0 = uniform(at.x), g1 = uniform(at.y);
-  const int before = kShared ? uniform(*a.prefix_count) : 0, last = before + g1 - g0;
-  if (!kShared && last == 0) return;  // one piece: written already
+  if (!kShared && g0 == g1) return;  // one piece: written already
   const int sub = 4 * wave + (lane >> 4);  // of the workgroup's 16 groups of lanes
   const int row = row0 + sub / spread;
   const int qrow = min(row, rows - 1), t = qrow / a.group;
+  // of the prefix's pieces for this row: how many, the first one's slot, and the slots from one to the next
+  int before = 0;
+  int64_t there = 0, apart = 0;
+  if constexpr (kShared) {
+    const int all = seq * rows + qrow;
+    if (a.large) {
+      PrefixCut cut = a.cut;
+      cut.cut((min(max(*a.prefix_len, 0), a.prefix_most) + kPrefixKeys - 1) / kPrefixKeys);
+      before = cut.count(all / kPrefixRows);
+      there = (head * cut.slots() + cut.slot(all / kPrefixRows)) * kPrefixRows + all % kPrefixRows;
+      apart = kPrefixRows;
+    } else {
+      before = *a.prefix_count;
+      apart = (int64_t)a.batch * rows;
+      there = head * a.prefix_G * apart + all;
+    }
+  }
+  const int last = before + g1 - g0;
   const int64_t slot0 = ((int64_t)head * a.row_tiles + qrow / C::kRows) * (2 * a.G + (kShared ? a.batch : 0));
   const bool whole = kShared && g0 == g1;  // a sequence in one piece
   const float end = a.part_ml[2 * ((slot0 + (whole ? 2 * a.G + seq : 2 * g1)) * C::kRows + qrow % C::kRows) + 1];
@@ -688,7 +644,7 @@ __global__ __launch_bounds__(256) void tree_attention_join_kernel(AttnArgs a) {
     for (int k = 0; k < kAtOnce; ++k) {
       const int gk = min(g + k * spread, last) - before;
       const bool shared = kShared && gk < 0;
-      const int64_t slot = shared ? ((int64_t)head * a.prefix_G + gk + before) * a.batch * rows + (int64_t)seq * rows + qrow
+      const int64_t slot = shared ? there + (gk + before) * apart
                                   : (slot0 + (whole ? 2 * a.G + seq : 2 * (g0 + gk) + (gk == 0 ? 1 : 0))) * C::kRows +
                                         qrow % C::kRows;
       const float* part_o = shared ? a.prefix_o : a.part_o;
@@ -868,12 +824,20 @@ SharedPlan plan_shared_attention(const CacheView& c, const CacheView& prefix, in
                                  int64_t D) {
   SharedPlan p{};
   p.own = plan_tree_attention(c, batch, T, group, D);
-  const AttnPlan all = plan_tree_attention(prefix, 1, batch * T, group, D);
-  p.prefix_tiles = all.row_tiles;
-  const int64_t units = all.row_tiles * c.kv_heads;
-  const int64_t most = cdiv((int64_t)prefix.table_width << prefix.page_shift, 32);  // tiles have 32 keys or more
-  p.prefix_parts = std::min(most, std::max<int64_t>(1, all.slots / units));
-  const int64_t rows = c.kv_heads * p.prefix_parts * batch * T * group;
+  const int64_t all_rows = batch * T * group;
+  int64_t rows;
+  p.large = all_rows > 128;
+  if (p.large) {
+    p.cut = PrefixCut::plan(cdiv(all_rows, kPrefixRows), std::max<int64_t>(1, 256 / c.kv_heads), prefix_pair(D));
+    rows = c.kv_heads * p.cut.slots() * kPrefixRows;
+    p.prefix_parts = p.cut.whole ? 1 : p.cut.parts;
+  } else {
+    const AttnPlan all = plan_tree_attention(prefix, 1, batch * T, group, D);
+    p.prefix_tiles = all.row_tiles;
+    const int64_t most = cdiv((int64_t)prefix.table_width << prefix.page_shift, 32);  // tiles have 32 keys or more
+    p.prefix_parts = std::min(most, std::max<int64_t>(1, all.slots / (all.row_tiles * c.kv_heads)));
+    rows = c.kv_heads * p.prefix_parts * all_rows;
+  }
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -906,17 +870,26 @@ hipError_t launch_shared_attention(const SharedPlan& p, const CacheView& c, cons
   a.prefix_G = (int)p.prefix_parts;
   const int64_t pieces = p.prefix_parts + cdiv(p.own.G, batch);
   a.spread = pieces >= 32 ? 16 : pieces >= 8 ? 4 : 1;
-  AttnArgs b = a;
-  b.c = prefix;
-  b.batch = 1;
-  b.T = (int)(batch * T);
-  b.nodes = 0;
-  b.G = b.prefix_G;
-  b.row_tiles = (int)p.prefix_tiles;
-  b.whole = false;
-  b.pieces = nullptr;
-  auto first = [&](auto cfg) { return launch<decltype(cfg), kPrefix>(b, stream); };
-  const hipError_t e = D == 64 ? with_cfg<64>(batch * T * group, first) : with_cfg<128>(batch * T * group, first);
+  a.large = p.large;
+  a.cut = p.cut;
+  a.prefix_len = prefix.lens;
+  a.prefix_most = prefix.table_width << prefix.page_shift;
+  hipError_t e;
+  if (p.large) {
+    e = launch_prefix_attention(prefix, p.cut, q, batch * T * group, group, D, a.c2, a.prefix_o, a.prefix_ml, stream);
+  } else {
+    AttnArgs b = a;
+    b.c = prefix;
+    b.batch = 1;
+    b.T = (int)(batch * T);
+    b.nodes = 0;
+    b.G = b.prefix_G;
+    b.row_tiles = (int)p.prefix_tiles;
+    b.whole = false;
+    b.pieces = nullptr;
+    auto first = [&](auto cfg) { return launch<decltype(cfg), kPrefix>(b, stream); };
+    e = D == 64 ? with_cfg<64>(batch * T * group, first) : with_cfg<128>(batch * T * group, first);
+  }
   if (e != hipSuccess) return e;
   auto then = [&](auto cfg) { return launch<decltype(cfg), kOwn>(a, stream); };
   return D == 64 ? with_cfg<64>(T * group, then) : with_cfg<128>(T * group, then);

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "prefix.h"
+
 namespace dfs {
 
 // Workgroups a launch should offer MI355X (256 CUs) to keep every CU busy.
@@ -259,10 +261,18 @@ hipError_t launch_tree_attention(const AttnPlan& p, const CacheView& c, const vo
                                  const void* v_new, const int32_t* parents, int64_t batch, int64_t T, int64_t group,
                                  int64_t D, double scale, void* out, void* ws, hipStream_t stream);
 
+constexpr int kPrefixKeys = 64;  // of a key tile of the prefix's kernel
+constexpr int kPrefixRows = 256;  // of a row tile of it
+inline int prefix_pair(int64_t D) { return D == 64 ? 2 : 1; }  // workgroups of it on a CU
+hipError_t launch_prefix_attention(const CacheView& prefix, const PrefixCut& cut, const void* q, int64_t rows,
+                                   int64_t group, int64_t D, float c2, float* part_o, float* part_ml,
+                                   hipStream_t stream);
 // The same over a prefix that the batch shares, `prefix` being its one-sequence cache.
 struct SharedPlan {
   AttnPlan own;            // of the sequences' own keys
-  int64_t prefix_parts;    // that the prefix is cut into, at most
+  bool large;              // the batch has rows enough for the prefix's own kernel,
+  PrefixCut cut;           // and its cut; otherwise tree attention's takes them:
+  int64_t prefix_parts;    // parts that the prefix is cut into, at most
   int64_t prefix_tiles;    // row tiles of the whole batch's rows
   size_t own_o, own_ml, pieces, prefix_o, prefix_ml, count;  // offsets in the workspace
   size_t ws_bytes;
