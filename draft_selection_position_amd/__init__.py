@@ -799,6 +799,7 @@ def tree_positions(parents: torch.Tensor, lens: torch.Tensor, prefix_len: torch.
 
 
 _LAYOUTS = {"half": 0, "interleaved": 1}
+_DENSE = torch.contiguous_format
 _SCALINGS = {None: 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 
 
@@ -817,18 +818,9 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
     return freqs if device is None else freqs.to(device), amplitude.value
 
 
-def _heads(t, what: str, dtype, index: int):
-    """(rows, heads, head_dim, values from a row to the next) of t [..., heads, head_dim], whose rows may lie apart (a
-    slice of a joint projection's heads), but evenly, and each in one piece."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.get_device() == index):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{what} must be a torch.Tensor")
-        if not t.is_cuda:
-            raise ValueError(f"{what} must be on a HIP device, got {t.device}")
-        if t.dtype is not dtype:
-            raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
-        raise ValueError(f"{what} must be on cuda:{index}, got {t.device}")
-    shape, step = t.shape, t.stride()
+def _rows_of(shape, step, what: str):
+    """(rows, heads, head_dim, values from a row to the next) of [..., heads, head_dim], whose rows may lie apart (a slice
+    of a joint projection's heads), but evenly, and each in one piece."""
     if len(shape) < 3:
         raise ValueError(f"{what} must be [..., heads, head_dim]")
     H, D = shape[-2:]
@@ -845,42 +837,60 @@ def _heads(t, what: str, dtype, index: int):
     return rows, H, D, apart
 
 
-def _rope_call(q, k, v, freqs, layout, amplitude, dtype, index):
-    """The struct of a call on q, k and v (any of them None), with rows and heads as they are given."""
+@functools.lru_cache(maxsize=1024)
+def _rope_shape(q, k, v, rot, layout, amplitude, dt):
+    """A call's sizes as the library takes them (a reference that is read during calls only), and its rows, kv heads and
+    head_dim.  q, k, v: (shape, strides), or None."""
     rows = D = None
     sizes = []
     for t, what in ((q, "q"), (k, "k"), (v, "v")):
         if t is None:
             sizes.append((0, 0))
             continue
-        n, H, d, apart = _heads(t, what, dtype, index)
+        n, H, d, apart = _rows_of(*t, what)
         if rows is None:
             rows, D = n, d
         elif (n, d) != (rows, D):
             raise ValueError(f"{what} must have {rows} tokens and heads of {D}")
         sizes.append((H, apart))
-    if k is not None and v is not None and k.shape != v.shape:
+    if k is not None and v is not None and k[0] != v[0]:
         raise ValueError("v must have the shape of k")
     if layout not in _LAYOUTS:
         raise ValueError(f"layout must be one of {list(_LAYOUTS)}, got {layout!r}")
-    rot = 0
-    if freqs is not None:
-        if not _fits(freqs, torch.float32, index):
-            _dev(freqs, "freqs", torch.float32)
-            raise ValueError(f"freqs must be on cuda:{index}, got {freqs.device}")
-        if freqs.dim() != 1:
-            raise ValueError("freqs must be [rot_dim / 2]")
-        rot = 2 * freqs.shape[0]
     (Hq, sq), (Hk, sk), (Hv, sv) = sizes
-    return _RopeShape(rows, Hq, Hk or Hv, D, rot, sq, sk, sv, amplitude, _LAYOUTS[layout], _CODES[dtype])
+    s = _RopeShape(rows, Hq, Hk or Hv, D, rot, sq, sk, sv, amplitude, _LAYOUTS[layout], dt)
+    return ctypes.byref(s), rows, Hk or Hv, D
 
 
-def _rope_dtype(t, what: str):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what} must be a torch.Tensor")
-    if t.dtype not in _CODES:
+def _on(t, dtype, index: int) -> bool:
+    """Whether t is a tensor of dtype on HIP device `index`."""
+    return isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.get_device() == index
+
+
+def _rope_lead(t, what: str):
+    """(dtype, its code, device index) of the tensor that the others of a call go by."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _CODES:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{what} must be a torch.Tensor")
         _dtype_code(t, what)
-    return t.dtype, t.get_device()
+    return t.dtype, _CODES[t.dtype], t.get_device()
+
+
+def _refuse_rope(lead, strided: dict, dense: dict, dtypes: dict) -> None:
+    """Raises for the first of the named tensors that is not on a HIP device, of its dtype and on lead's device, and for
+    those of `dense` not contiguous.  None of them is optional."""
+    for what, t in (strided | dense).items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{what} must be a torch.Tensor")
+    for what, t in (strided | dense).items():
+        if not t.is_cuda:
+            raise ValueError(f"{what} must be on a HIP device, got {t.device}")
+        if t.dtype != dtypes[what]:
+            raise ValueError(f"{what} must be {dtypes[what]}, got {t.dtype}")
+        if t.device != lead.device:
+            raise ValueError(f"{what} must be on {lead.device}, got {t.device}")
+        if what in dense and not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous")
 
 
 def rope(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None, positions: torch.Tensor,
@@ -891,20 +901,25 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None,
     in ``qkv.view(B, T, -1, D)[:, :, :q_heads]``; positions int32, one for each token (``tree_positions`` for drafted
     nodes); freqs and amplitude as ``rope_frequencies`` gives them.  ``layout`` "half" or "interleaved".  ``out`` may
     pass preallocated (q, k, v), which for dense q and k may be these themselves."""
-    lead = q if q is not None else k
+    lead = k if q is None else q
     if lead is None:
         raise ValueError("q or k must be given")
-    dtype, index = _rope_dtype(lead, "q" if q is not None else "k")
-    if freqs is None:
-        raise TypeError("freqs must be a torch.Tensor")
-    s = _rope_call(q, k, v, freqs, layout, amplitude, dtype, index)
-    if not _fits(positions, torch.int32, index):
-        _dev(positions, "positions", torch.int32)
-        raise ValueError(f"positions must be on cuda:{index}, got {positions.device}")
-    if positions.numel() != s.rows:
-        raise ValueError(f"positions must be one for each of {s.rows} tokens")
+    dtype, dt, index = _rope_lead(lead, "k" if q is None else "q")
+    if not (_fits(positions, torch.int32, index) and _fits(freqs, torch.float32, index) and _on(lead, dtype, index)
+            and (k is None or _on(k, dtype, index)) and (v is None or _on(v, dtype, index))):
+        given = {n: t for n, t in (("q", q), ("k", k), ("v", v)) if t is not None}
+        _refuse_rope(lead, given, {"positions": positions, "freqs": freqs},
+                     dict.fromkeys("qkv", dtype) | {"positions": torch.int32, "freqs": torch.float32})
+    if freqs.dim() != 1:
+        raise ValueError("freqs must be [rot_dim / 2]")
+    s, rows, _, _ = _rope_shape(None if q is None else (q.shape, q.stride()), None if k is None else (k.shape, k.stride()),
+                                None if v is None else (v.shape, v.stride()), 2 * freqs.shape[0], layout, amplitude, dt)
+    if positions.numel() != rows:
+        raise ValueError(f"positions must be one for each of {rows} tokens")
     if out is None:
-        out = tuple(None if t is None else torch.empty(t.shape, dtype=dtype, device=t.device) for t in (q, k, v))
+        oq = None if q is None else torch.empty_like(q, memory_format=_DENSE)
+        ok = None if k is None else torch.empty_like(k, memory_format=_DENSE)
+        ov = None if v is None else torch.empty_like(v, memory_format=_DENSE)
     else:
         if len(out) != 3:
             raise ValueError("out must be (q, k, v)")
@@ -913,9 +928,9 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None,
                 raise ValueError(f"out must hold {what} if and only if {what} is given")
             if o is not None and not (_fits(o, dtype, index) and o.shape == t.shape):
                 raise ValueError(f"out's {what} must be a contiguous {dtype} tensor of {what}'s shape on cuda:{index}")
-    oq, ok, ov = out
-    _call(index, "dfs_rope", lib().dfs_rope, _ptr(q), _ptr(k), _ptr(v), positions.data_ptr(), freqs.data_ptr(),
-          ctypes.byref(s), _ptr(oq), _ptr(ok), _ptr(ov))
+        oq, ok, ov = out
+    _call(index, "dfs_rope", lib().dfs_rope, _ptr(q), _ptr(k), _ptr(v), positions.data_ptr(), freqs.data_ptr(), s, _ptr(oq),
+          _ptr(ok), _ptr(ov))
     return oq, ok, ov
 
 
@@ -931,24 +946,27 @@ def cache_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, start
     freqs None: nothing is turned.  Writes the pools in place.  Returns (turned q or None, new lengths); rows of
     q that belong to no sequence are left as ``q_out`` holds them."""
     i32 = torch.int32
-    dtype, index = _rope_dtype(k, "k")
-    if v is None:
-        raise TypeError("v must be a torch.Tensor")
-    s = _rope_call(q, k, v, freqs, layout, amplitude, dtype, index)
-    if not (_fits(k_pages, dtype, index) and _fits(v_pages, dtype, index) and _fits(starts, i32, index)
+    dtype, dt, index = _rope_lead(k, "k")
+    if not (_on(k, dtype, index) and _on(v, dtype, index) and (q is None or _on(q, dtype, index))
+            and _fits(k_pages, dtype, index) and _fits(v_pages, dtype, index) and _fits(starts, i32, index)
             and _fits(block_table, i32, index) and _fits(lens, i32, index)
+            and (freqs is None or _fits(freqs, torch.float32, index))
             and (prefix_len is None or _fits(prefix_len, i32, index)) and (q_out is None or _fits(q_out, dtype, index))
             and (out_lens is None or _fits(out_lens, i32, index))):
-        given = {"k_pages": k_pages, "v_pages": v_pages, "starts": starts, "block_table": block_table, "lens": lens,
-                 "prefix_len": prefix_len, "q_out": q_out, "out_lens": out_lens}
-        given = {n: t for n, t in given.items() if n not in ("prefix_len", "q_out", "out_lens") or t is not None}
-        _refuse("k_pages", given, dict.fromkeys(given, i32) | {"k_pages": dtype, "v_pages": dtype, "q_out": dtype})
-        raise ValueError(f"the pools must be on cuda:{index}, got {k_pages.device}")
-    pages, table = k_pages.shape, block_table.shape
-    if len(pages) != 4 or v_pages.shape != pages or pages[1] != s.kv_heads or pages[3] != s.head_dim:
-        raise ValueError(f"k_pages and v_pages must both be [n_pages, {s.kv_heads}, page_size, {s.head_dim}]")
-    batch = lens.shape[0] if lens.dim() == 1 else -1
-    if len(table) != 2 or table[0] != batch or starts.shape != (batch + 1,):
+        dense = {"starts": starts, "k_pages": k_pages, "v_pages": v_pages, "block_table": block_table, "lens": lens}
+        more = {"freqs": freqs, "prefix_len": prefix_len, "q_out": q_out, "out_lens": out_lens}
+        _refuse_rope(k, {"k": k, "v": v} | ({} if q is None else {"q": q}),
+                     dense | {n: t for n, t in more.items() if t is not None},
+                     dict.fromkeys((*dense, *more), i32) | dict.fromkeys(("q", "k", "v", "k_pages", "v_pages", "q_out"), dtype)
+                     | {"freqs": torch.float32})
+    if freqs is not None and freqs.dim() != 1:
+        raise ValueError("freqs must be [rot_dim / 2]")
+    s, _, Hkv, D = _rope_shape(None if q is None else (q.shape, q.stride()), (k.shape, k.stride()), (v.shape, v.stride()),
+                               0 if freqs is None else 2 * freqs.shape[0], layout, amplitude, dt)
+    pages, table, batch = k_pages.shape, block_table.shape, lens.shape
+    if len(pages) != 4 or v_pages.shape != pages or pages[1] != Hkv or pages[3] != D:
+        raise ValueError(f"k_pages and v_pages must both be [n_pages, {Hkv}, page_size, {D}]")
+    if len(batch) != 1 or len(table) != 2 or table[0] != batch[0] or starts.shape != (batch[0] + 1,):
         raise ValueError("lens must be [batch], block_table [batch, width] and starts [batch + 1]")
     if prefix_len is not None and prefix_len.numel() != 1:
         raise ValueError("prefix_len must be [1]")
@@ -956,17 +974,17 @@ def cache_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, start
         if q_out is not None:
             raise ValueError("q_out needs a q")
     elif q_out is None:
-        q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        q_out = torch.empty_like(q, memory_format=_DENSE)
     elif q_out.shape != q.shape:
         raise ValueError("q_out must have the shape of q")
     if out_lens is None:
         out_lens = torch.empty_like(lens)
-    elif out_lens.shape != lens.shape:
+    elif out_lens.shape != batch:
         raise ValueError("out_lens must be [batch]")
-    c, _ = _cache_shape(batch, 1, s.kv_heads, s.kv_heads, s.head_dim, pages[2], pages[0], table[1], s.dtype)
+    c, _ = _cache_shape(batch[0], 1, Hkv, Hkv, D, pages[2], pages[0], table[1], dt)
     _call(index, "dfs_cache_append", lib().dfs_cache_append, _ptr(q), k.data_ptr(), v.data_ptr(), starts.data_ptr(),
-          _ptr(freqs), ctypes.byref(s), _ptr(prefix_len), _ptr(q_out), k_pages.data_ptr(), v_pages.data_ptr(),
-          block_table.data_ptr(), lens.data_ptr(), c, out_lens.data_ptr())
+          _ptr(freqs), s, _ptr(prefix_len), _ptr(q_out), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+          lens.data_ptr(), c, out_lens.data_ptr())
     return q_out, out_lens
 
 
