@@ -30,7 +30,9 @@
 // card holds 2.0 GHz under it.  One token, 4001 keys: 12.0 us, two launches and a chain of four
 // memory latencies (lengths, pages, keys, pieces); its 16 MB would take 2.5.
 #include <algorithm>
+#include <type_traits>
 
+#include "../../include/dfs.h"
 #include "attn_tile.h"
 #include "dfs_internal.h"
 
@@ -39,8 +41,8 @@ namespace {
 
 constexpr float kUnused = -1.0f;  // for a sum of weights
 
-// What a workgroup's keys are: a sequence's cache and tree, the whole answer; the same of a batch with a shared
-// prefix, whose part of the answer is still to be joined with the prefix's; or the prefix, for the rows of the whole
+// What a workgroup's keys are.  kTree: a sequence's cache and tree, the whole answer.  Of a batch with a shared prefix:
+// kOwn the same, but a piece of the answer, to be joined with the prefix's; kPrefix the prefix, for the rows of the whole
 // batch as the one sequence that it is (no node is a key then, and every row sees all).
 enum Role { kTree, kOwn, kPrefix };
 
@@ -51,7 +53,8 @@ struct AttnArgs {
   const uint16_t* v_new;
   const int32_t* parents;
   uint16_t* out;
-  float* part_o;   // [Hkv, row tiles, 2 G, rows of a tile, D]; kOwn: 2 G + batch, the last for sequences in one piece
+  float* part_o;   // [Hkv, row tiles, 2 G, rows of a tile, D]; kOwn: cut_slots (2 G, or none of parts that are
+                   // sequences) and one for each sequence that is in one piece, of slot_rows
   float* part_ml;  // [Hkv, row tiles, 2 G, rows of a tile, 2]: maximum and sum; of an unused node's row the last piece has kUnused
   int2* pieces;    // [batch]: the first and the last part with a tile of the sequence (NULL: nothing to join)
   // a shared prefix's pieces: [Hkv, slots, rows of a tile, D] as the prefix's own kernel leaves them, or by tree
@@ -66,6 +69,8 @@ struct AttnArgs {
   int prefix_G;
   int batch, T, group, G, row_tiles;
   int nodes;  // of a sequence that are keys: T, or none of the prefix
+  int cut_slots;
+  int slot_rows;  // kOwn: of a slot, as many as there are where one tile has them all
   bool whole;  // parts are sequences
   int spread;  // 16-lane groups that join a row's pieces: 1, 4 or 16
   float c2;  // scale * log2(e)
@@ -300,19 +305,43 @@ __device__ __forceinline__ void group_sync() {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 }
 
+// Of a row of a batch with a shared prefix, numbered through the batch: the prefix's pieces, how many there are, the first
+// one's slot, and the slots from one to the next.
+struct PrefixPieces {
+  int n;
+  int64_t first, apart;
+};
+__device__ __forceinline__ PrefixPieces prefix_pieces(const AttnArgs& a, int head, int row) {
+  if (!a.large) {
+    const int64_t rows = (int64_t)a.batch * a.T * a.group;
+    return PrefixPieces{*a.prefix_count, head * a.prefix_G * rows + row, rows};
+  }
+  PrefixCut cut = a.cut;
+  cut.cut((min(max(*a.prefix_len, 0), a.prefix_most) + kPrefixKeys - 1) / kPrefixKeys);
+  const int rt = row / kPrefixRows;
+  return PrefixPieces{cut.count(rt), (head * cut.slots() + cut.slot(rt)) * kPrefixRows + row % kPrefixRows, kPrefixRows};
+}
+
+template <class C>
+struct Shared {
+  char lds[C::kLds];
+  int scratch[C::kThreads + 2];
+  int s_odd[C::KW];
+};
+
 template <class C, Role kRole>
-__global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kernel(AttnArgs a) {
-  __shared__ __attribute__((aligned(1024))) char lds[C::kLds];
-  __shared__ int scratch[C::kThreads + 2];
-  __shared__ int s_odd[C::KW];
+__device__ __forceinline__ void attend(const AttnArgs& a, int block, Shared<C>& shared) {
+  char* const lds = shared.lds;
+  int* const scratch = shared.scratch;
+  int* const s_odd = shared.s_odd;
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
   const int kw = wave / C::RW, rw = wave % C::RW;
   const int Hkv = a.c.kv_heads;
   // Workgroups go round the eight XCDs in turn: the row tiles of a part are eight apart, so
   // that they run side by side on one XCD and read the part's keys into its L2 once.
-  const int turn = blockIdx.x / (8 * a.row_tiles), rt = blockIdx.x / 8 % a.row_tiles;
-  const int unit = turn * 8 + blockIdx.x % 8;  // (head, part)
+  const int turn = block / (8 * a.row_tiles), rt = block / 8 % a.row_tiles;
+  const int unit = turn * 8 + block % 8;  // (head, part)
   if (unit >= Hkv * a.G) return;
   const int head = unit / a.G, g = unit % a.G;
   // part g: the tiles x .. x_end - 1, at least one
@@ -336,7 +365,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
   const int row = rt * C::kRows + 32 * rw + (lane & 31);
   const int qrow = min(row, rows - 1), t = qrow / a.group, gh = qrow % a.group;
   const int h = lane >> 5;
-  const int64_t slot0 = ((int64_t)head * a.row_tiles + rt) * (2 * a.G + (kRole == kOwn ? a.batch : 0));
+  const int64_t slot0 = ((int64_t)head * a.row_tiles + rt) * (kRole == kOwn ? a.cut_slots + a.batch : 2 * a.G);
   const Frag<C> at(lane);
   const uint32_t ring0 = lds_addr(lds) + kw * C::S * C::kStage;
   const uint32_t pages0 = lds_addr(lds) + C::kRing + wave * (C::kAhead + 1) * C::kPages;
@@ -571,10 +600,11 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
           *reinterpret_cast<uint2*>(a.out + qoff + d0 + 8 * u) = pk.u;
         }
       } else {
-        const int64_t slot = kRole == kPrefix ? ((int64_t)head * a.prefix_G + g) * rows + row
-                                              : (slot0 + (kRole == kOwn && first == 0 && last == tiles ? 2 * a.G + seq
-                                                                                                     : 2 * g + (first == 0 ? 1 : 0))) *
-                                                        C::kRows + 32 * rw + (lane & 31);
+        const int64_t slot =
+            kRole == kPrefix ? ((int64_t)head * a.prefix_G + g) * rows + row
+            : kRole == kOwn  ? (slot0 + (first == 0 && last == tiles ? a.cut_slots + seq : 2 * g + (first == 0 ? 1 : 0))) * a.slot_rows +
+                                  32 * rw + (lane & 31)
+                             : (slot0 + 2 * g + (first == 0 ? 1 : 0)) * C::kRows + 32 * rw + (lane & 31);
         float* part_o = kRole == kPrefix ? a.prefix_o : a.part_o;
         float* part_ml = kRole == kPrefix ? a.prefix_ml : a.part_ml;
 #pragma unroll
@@ -588,6 +618,22 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kern
     before += tiles;
     ++seq;
   }
+}
+
+template <class C, Role kRole>
+__global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tree_attention_kernel(AttnArgs a) {
+  __shared__ __attribute__((aligned(1024))) Shared<C> shared;
+  attend<C, kRole>(a, blockIdx.x, shared);
+}
+
+// The prefix for few rows, by the first n workgroups, and the sequences' own keys beside it.
+template <class C>
+__global__ __launch_bounds__(C::kThreads, C::kMinWaves) void beside_prefix_kernel(AttnArgs prefix, AttnArgs own, int n) {
+  __shared__ __attribute__((aligned(1024))) Shared<C> shared;
+  if ((int)blockIdx.x < n)
+    attend<C, kPrefix>(prefix, blockIdx.x, shared);
+  else
+    attend<C, kOwn>(own, blockIdx.x - n, shared);
 }
 
 // Sequences cut over several workgroups: their pieces joined.  16 lanes hold a row's D
@@ -613,27 +659,13 @@ __global__ __launch_bounds__(256) void tree_attention_join_kernel(AttnArgs a) {
   const int sub = 4 * wave + (lane >> 4);  // of the workgroup's 16 groups of lanes
   const int row = row0 + sub / spread;
   const int qrow = min(row, rows - 1), t = qrow / a.group;
-  // of the prefix's pieces for this row: how many, the first one's slot, and the slots from one to the next
-  int before = 0;
-  int64_t there = 0, apart = 0;
-  if constexpr (kShared) {
-    const int all = seq * rows + qrow;
-    if (a.large) {
-      PrefixCut cut = a.cut;
-      cut.cut((min(max(*a.prefix_len, 0), a.prefix_most) + kPrefixKeys - 1) / kPrefixKeys);
-      before = cut.count(all / kPrefixRows);
-      there = (head * cut.slots() + cut.slot(all / kPrefixRows)) * kPrefixRows + all % kPrefixRows;
-      apart = kPrefixRows;
-    } else {
-      before = *a.prefix_count;
-      apart = (int64_t)a.batch * rows;
-      there = head * a.prefix_G * apart + all;
-    }
-  }
+  const PrefixPieces of = kShared ? prefix_pieces(a, head, seq * rows + qrow) : PrefixPieces{};
+  const int before = of.n;
   const int last = before + g1 - g0;
-  const int64_t slot0 = ((int64_t)head * a.row_tiles + qrow / C::kRows) * (2 * a.G + (kShared ? a.batch : 0));
+  const int64_t slot0 = ((int64_t)head * a.row_tiles + qrow / C::kRows) * (kShared ? a.cut_slots + a.batch : 2 * a.G);
   const bool whole = kShared && g0 == g1;  // a sequence in one piece
-  const float end = a.part_ml[2 * ((slot0 + (whole ? 2 * a.G + seq : 2 * g1)) * C::kRows + qrow % C::kRows) + 1];
+  const int slot_rows = kShared ? a.slot_rows : C::kRows;
+  const float end = a.part_ml[2 * ((slot0 + (whole ? a.cut_slots + seq : 2 * g1)) * slot_rows + qrow % C::kRows) + 1];
   float m = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) o[e] = 0.f;
@@ -644,8 +676,8 @@ __global__ __launch_bounds__(256) void tree_attention_join_kernel(AttnArgs a) {
     for (int k = 0; k < kAtOnce; ++k) {
       const int gk = min(g + k * spread, last) - before;
       const bool shared = kShared && gk < 0;
-      const int64_t slot = shared ? there + (gk + before) * apart
-                                  : (slot0 + (whole ? 2 * a.G + seq : 2 * (g0 + gk) + (gk == 0 ? 1 : 0))) * C::kRows +
+      const int64_t slot = shared ? of.first + (gk + before) * of.apart
+                                  : (slot0 + (whole ? a.cut_slots + seq : 2 * (g0 + gk) + (gk == 0 ? 1 : 0))) * slot_rows +
                                         qrow % C::kRows;
       const float* part_o = shared ? a.prefix_o : a.part_o;
       const float* part_ml = shared ? a.prefix_ml : a.part_ml;
@@ -726,14 +758,24 @@ __global__ __launch_bounds__(256) void tree_attention_join_kernel(AttnArgs a) {
   for (int e = 0; e < kPer / 4; ++e) reinterpret_cast<uint2*>(out)[e] = pk.u[e];
 }
 
-template <class C, Role kRole>
-hipError_t launch(const AttnArgs& a, hipStream_t stream) {
-  tree_attention_kernel<C, kRole><<<dim3((uint32_t)(cdiv((int64_t)a.G * a.c.kv_heads, 8) * 8 * a.row_tiles)), dim3(C::kThreads), 0, stream>>>(a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.pieces) return e;
-  tree_attention_join_kernel<C, kRole == kOwn><<<
+template <class C>
+uint32_t blocks_of(const AttnArgs& a) {
+  return (uint32_t)(cdiv((int64_t)a.G * a.c.kv_heads, 8) * 8 * a.row_tiles);
+}
+
+template <class C, bool kShared>
+hipError_t launch_join(const AttnArgs& a, hipStream_t stream) {
+  tree_attention_join_kernel<C, kShared><<<
       dim3((uint32_t)(a.batch * a.c.kv_heads * cdiv(a.T * a.group, 16 / a.spread))), dim3(256), 0, stream>>>(a);
   return hipGetLastError();
+}
+
+template <class C, Role kRole>
+hipError_t launch(const AttnArgs& a, hipStream_t stream) {
+  tree_attention_kernel<C, kRole><<<dim3(blocks_of<C>(a)), dim3(C::kThreads), 0, stream>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.pieces || kRole == kPrefix) return e;
+  return launch_join<C, kRole == kOwn>(a, stream);
 }
 
 // Query rows of a head, and the configurations that take them: up to 32 the waves have keys
@@ -756,9 +798,36 @@ auto with_cfg(int64_t rows, F f) {
 
 }  // namespace
 
-AttnPlan plan_tree_attention(const CacheView& c, int64_t batch, int64_t T, int64_t group, int64_t D) {
+namespace {
+
+// How a batch goes over its shared prefix.  Few rows or few products: tree attention's kernel, in one launch with the
+// sequences' own keys, so that the call is two launches.  From 3 x 2^32 products of a kind on (rows x heads x the
+// prefix's longest x D), and more than 384 rows: the prefix's own kernel, which is half as fast again but fills
+// slowly and takes tiles of 256 rows (us, own kernel against the other: 512 rows x 8 heads of 128 x 32768 keys 99 and 106, 4352 x
+// 8 x 8000 190 and 238, 4352 x 8 of 64 x 8000 113 and 158; below, 768 x 8 x 16384 94 and 98, 1020 x 4 x 16384 83 and 66,
+// 544 x 8 x 1000 44 and 28; 384 x 8 x 65536 179 and 171).
+bool prefix_is_large(int64_t rows, int64_t kv_heads, int64_t D, int64_t longest) {
+  return rows > 384 && (double)rows * (double)kv_heads * (double)D * (double)longest >= 3.0 * 4294967296.0;
+}
+// In one launch the own keys go by the rows of the whole batch, in tiles that one sequence's rows do not fill: up to so many
+// keys the saved launch pays (16 tokens x 8 heads x 4 of 128, 4001 keys, own 77: 21.2 us against 29.5, 4000: 48 and 51, 8000: 75
+// and 71, 16000: 121 and 107; 40 tokens x 2 x 4 of 64, 8000: 32 and 36, 16000: 50 and 46).
+constexpr int64_t kBesideKeys = 8192;
+// Otherwise, up to 32 rows of a sequence and head, 1024 of these or more and no long one: a wave for each, four or
+// more of them on a CU, where a workgroup that goes through several in turn waits for each one's start (256 tokens x 8 x 4 of 128,
+// up to 100 own keys: 64 us a call against 96, up to 1024: 194 and 206; 256 x 4 x 8, up to 2000: 145 both).
+bool own_by_waves(int64_t rows, int64_t pairs, int64_t longest) { return rows <= 32 && pairs >= 1024 && longest <= 2048; }
+
+template <int D, class F>
+auto with_own_cfg(int64_t rows, bool single, F f) {
+  if (single) return f(Cfg<D, 1, 1, 2, 1>{});
+  return with_cfg<D>(rows, f);
+}
+
+template <class F>
+AttnPlan plan_attention(const CacheView& c, int64_t batch, int64_t T, int64_t group, int64_t D, bool whole, F with) {
   const int64_t rows = T * group;
-  auto plan = [&](auto cfg) {
+  return with([&](auto cfg) {
     typedef decltype(cfg) C;
     AttnPlan p{};
     p.row_tiles = cdiv(rows, C::kRows);
@@ -771,7 +840,7 @@ AttnPlan plan_tree_attention(const CacheView& c, int64_t batch, int64_t T, int64
     // keys cuts sequences however short they are): a part for each and no join (4 x 9 nodes, page 256: 8.0 us
     // against 10.2; 39 x 33 nodes, up to 61 keys: 17.8 against 24.4; 13 x 56 nodes, 7 heads, 243 keys: 16.2
     // against 27.9; at worst 2 x 18 nodes, 3 heads, 115 keys: 14.0 against 12.8).
-    p.whole = each <= 4 || (each <= 8 && batch * c.kv_heads * p.row_tiles >= 48);
+    p.whole = whole || each <= 4 || (each <= 8 && batch * c.kv_heads * p.row_tiles >= 48);
     if (p.whole) p.G = batch;
     p.tile_rows = C::kRows;
     const int64_t rows = (int64_t)c.kv_heads * p.row_tiles * 2 * p.G * C::kRows;
@@ -780,8 +849,15 @@ AttnPlan plan_tree_attention(const CacheView& c, int64_t batch, int64_t T, int64
     p.ml_bytes = join ? align_up((size_t)rows * 8, 256) : 0;
     p.ws_bytes = join ? p.part_bytes + p.ml_bytes + align_up((size_t)batch * 8, 256) : 0;
     return p;
-  };
-  return D == 64 ? with_cfg<64>(rows, plan) : with_cfg<128>(rows, plan);
+  });
+}
+
+}  // namespace
+
+AttnPlan plan_tree_attention(const CacheView& c, int64_t batch, int64_t T, int64_t group, int64_t D) {
+  return plan_attention(c, batch, T, group, D, false, [&](auto plan) {
+    return D == 64 ? with_cfg<64>(T * group, plan) : with_cfg<128>(T * group, plan);
+  });
 }
 
 namespace {
@@ -823,34 +899,44 @@ hipError_t launch_tree_attention(const AttnPlan& p, const CacheView& c, const vo
 SharedPlan plan_shared_attention(const CacheView& c, const CacheView& prefix, int64_t batch, int64_t T, int64_t group,
                                  int64_t D) {
   SharedPlan p{};
-  p.own = plan_tree_attention(c, batch, T, group, D);
   const int64_t all_rows = batch * T * group;
-  int64_t rows;
-  p.large = all_rows > 128;
-  if (p.large) {
-    p.cut = PrefixCut::plan(cdiv(all_rows, kPrefixRows), std::max<int64_t>(1, 256 / c.kv_heads), prefix_pair(D));
-    rows = c.kv_heads * p.cut.slots() * kPrefixRows;
-    p.prefix_parts = p.cut.whole ? 1 : p.cut.parts;
-  } else {
-    const AttnPlan all = plan_tree_attention(prefix, 1, batch * T, group, D);
-    p.prefix_tiles = all.row_tiles;
-    const int64_t most = cdiv((int64_t)prefix.table_width << prefix.page_shift, 32);  // tiles have 32 keys or more
-    p.prefix_parts = std::min(most, std::max<int64_t>(1, all.slots / (all.row_tiles * c.kv_heads)));
-    rows = c.kv_heads * p.prefix_parts * all_rows;
-  }
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
     off += align_up(bytes, 256);
     return at;
   };
-  const int64_t own_rows = c.kv_heads * p.own.row_tiles * (2 * p.own.G + batch) * p.own.tile_rows;
+  int64_t rows;
+  const int64_t longest = (int64_t)c.table_width << c.page_shift, prefix_longest = (int64_t)prefix.table_width << prefix.page_shift;
+  p.large = prefix_is_large(all_rows, c.kv_heads, D, prefix_longest);
+  p.single = own_by_waves(T * group, batch * c.kv_heads, longest);
+  p.beside = !p.large && !p.single && longest <= kBesideKeys;
+  p.cfg_rows = p.beside ? all_rows : T * group;
+  p.own = plan_attention(c, batch, T, group, D, p.single, [&](auto plan) {
+    return D == 64 ? with_own_cfg<64>(p.cfg_rows, p.single, plan) : with_own_cfg<128>(p.cfg_rows, p.single, plan);
+  });
+  if (p.large) {
+    p.cut = PrefixCut::plan(cdiv(all_rows, kPrefixRows), std::max<int64_t>(1, 256 / c.kv_heads), prefix_pair(D));
+    rows = c.kv_heads * p.cut.slots() * kPrefixRows;
+    p.prefix_parts = p.cut.pair * (p.cut.whole ? 1 : p.cut.parts);
+  } else {
+    const AttnPlan all = plan_tree_attention(prefix, 1, batch * T, group, D);
+    p.prefix_tiles = all.row_tiles;
+    const int64_t most = cdiv(prefix_longest, 32);  // tiles have 32 keys or more
+    // both in one launch, where they fit
+    const int64_t slots = !p.beside ? all.slots : std::max<int64_t>(all.slots / 2, all.slots - p.own.G * p.own.row_tiles * c.kv_heads);
+    p.prefix_parts = std::min(most, std::max<int64_t>(1, slots / (all.row_tiles * c.kv_heads)));
+    rows = c.kv_heads * p.prefix_parts * all_rows;
+    p.count = take(4);
+  }
+  p.cut_slots = p.own.whole ? 0 : 2 * p.own.G;
+  p.slot_rows = p.own.row_tiles == 1 ? T * group : p.own.tile_rows;
+  const int64_t own_rows = c.kv_heads * p.own.row_tiles * (p.cut_slots + batch) * p.slot_rows;
   p.own_o = take((size_t)(own_rows * D) * 4);
   p.own_ml = take((size_t)own_rows * 8);
   p.pieces = take((size_t)batch * 8);
   p.prefix_o = take((size_t)(rows * D) * 4);
   p.prefix_ml = take((size_t)rows * 8);
-  p.count = take(4);
   p.ws_bytes = off;
   return p;
 }
@@ -866,33 +952,47 @@ hipError_t launch_shared_attention(const SharedPlan& p, const CacheView& c, cons
   a.pieces = reinterpret_cast<int2*>(w + p.pieces);
   a.prefix_o = reinterpret_cast<float*>(w + p.prefix_o);
   a.prefix_ml = reinterpret_cast<float*>(w + p.prefix_ml);
-  a.prefix_count = reinterpret_cast<int*>(w + p.count);
-  a.prefix_G = (int)p.prefix_parts;
-  const int64_t pieces = p.prefix_parts + cdiv(p.own.G, batch);
-  a.spread = pieces >= 32 ? 16 : pieces >= 8 ? 4 : 1;
   a.large = p.large;
   a.cut = p.cut;
   a.prefix_len = prefix.lens;
   a.prefix_most = prefix.table_width << prefix.page_shift;
-  hipError_t e;
+  a.prefix_G = (int)p.prefix_parts;
+  a.cut_slots = (int)p.cut_slots;
+  a.slot_rows = (int)p.slot_rows;
+  const int64_t pieces = p.prefix_parts + cdiv(p.own.G, batch);
+  // by a row's pieces, but no more workgroups than help (16 rows x 8 heads, 28 pieces: 14.2 us a call by 16 against 16.5 by 4;
+  // 128 x 8 x 4 rows, 17 pieces: 96 by 4 against 107)
+  a.spread = pieces < 8 ? 1 : batch * T * group * c.kv_heads <= 2048 ? 16 : 4;
   if (p.large) {
-    e = launch_prefix_attention(prefix, p.cut, q, batch * T * group, group, D, a.c2, a.prefix_o, a.prefix_ml, stream);
-  } else {
-    AttnArgs b = a;
-    b.c = prefix;
-    b.batch = 1;
-    b.T = (int)(batch * T);
-    b.nodes = 0;
-    b.G = b.prefix_G;
-    b.row_tiles = (int)p.prefix_tiles;
-    b.whole = false;
-    b.pieces = nullptr;
-    auto first = [&](auto cfg) { return launch<decltype(cfg), kPrefix>(b, stream); };
-    e = D == 64 ? with_cfg<64>(batch * T * group, first) : with_cfg<128>(batch * T * group, first);
+    const hipError_t e = launch_prefix_attention(prefix, p.cut, q, batch * T * group, group, D, a.c2, a.prefix_o, a.prefix_ml, stream);
+    if (e != hipSuccess) return e;
+    auto own = [&](auto cfg) { return launch<decltype(cfg), kOwn>(a, stream); };
+    return D == 64 ? with_own_cfg<64>(T * group, p.single, own) : with_own_cfg<128>(T * group, p.single, own);
   }
-  if (e != hipSuccess) return e;
-  auto then = [&](auto cfg) { return launch<decltype(cfg), kOwn>(a, stream); };
-  return D == 64 ? with_cfg<64>(T * group, then) : with_cfg<128>(T * group, then);
+  a.prefix_count = reinterpret_cast<int*>(w + p.count);
+  AttnArgs b = a;
+  b.c = prefix;
+  b.batch = 1;
+  b.T = (int)(batch * T);
+  b.nodes = 0;
+  b.G = b.prefix_G;
+  b.row_tiles = (int)p.prefix_tiles;
+  b.whole = false;
+  b.pieces = nullptr;
+  auto run = [&](auto cfg) {
+    typedef decltype(cfg) C;
+    if (!p.beside) {
+      const hipError_t e = launch<C, kPrefix>(b, stream);
+      if (e != hipSuccess) return e;
+      auto own = [&](auto cfg) { return launch<decltype(cfg), kOwn>(a, stream); };
+      return with_own_cfg<C::D>(T * group, p.single, own);
+    }
+    const uint32_t n = blocks_of<C>(b);
+    beside_prefix_kernel<C><<<dim3(n + blocks_of<C>(a)), dim3(C::kThreads), 0, stream>>>(b, a, (int)n);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : launch_join<C, true>(a, stream);
+  };
+  return D == 64 ? with_cfg<64>(batch * T * group, run) : with_cfg<128>(batch * T * group, run);
 }
 
 }  // namespace dfs

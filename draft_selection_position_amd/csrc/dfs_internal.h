@@ -269,11 +269,16 @@ hipError_t launch_prefix_attention(const CacheView& prefix, const PrefixCut& cut
                                    hipStream_t stream);
 // The same over a prefix that the batch shares, `prefix` being its one-sequence cache.
 struct SharedPlan {
-  AttnPlan own;            // of the sequences' own keys
-  bool large;              // the batch has rows enough for the prefix's own kernel,
-  PrefixCut cut;           // and its cut; otherwise tree attention's takes them:
-  int64_t prefix_parts;    // parts that the prefix is cut into, at most
-  int64_t prefix_tiles;    // row tiles of the whole batch's rows
+  AttnPlan own;          // of the sequences' own keys
+  bool large;            // the batch has rows enough for the prefix's own kernel,
+  PrefixCut cut;         // with its cut,
+  bool single;           // and sequences enough for a wave each; otherwise tree attention's kernel takes the prefix:
+  bool beside;           // one launch for both, in the prefix's configuration
+  int64_t cfg_rows;      // the rows that the own keys' configuration goes by
+  int64_t prefix_parts;  // parts that it is cut into, at most
+  int64_t prefix_tiles;  // row tiles of the whole batch's rows
+  int64_t cut_slots;     // for pieces of sequences that are cut
+  int64_t slot_rows;     // of a slot for own pieces
   size_t own_o, own_ml, pieces, prefix_o, prefix_ml, count;  // offsets in the workspace
   size_t ws_bytes;
 };

@@ -15,7 +15,7 @@ namespace dfs {
 // Where a CU holds two workgroups (`pair` 2), two share a range.  The one that started first is served first, and gets on
 // that much faster: it takes kFirst / 64 of the range's key tiles.
 struct PrefixCut {
-  static constexpr int kFirst = 40, kStart = 4, kLeast = 8;  // key tiles; a range or a part has no fewer than kLeast
+  static constexpr int kFirst = 40, kStart = 4, kLeast = 2;  // key tiles; a range or a part has no fewer than kLeast
   int pair, C, whole, n, f, e, parts;  // on the host: from row tiles and C; parts: ranges of one of the n at most
   int tiles, each, rest;         // on the device: from the prefix's length; `rest` of a row tile is shared,
   int64_t share;                 // so much of it by one of the e

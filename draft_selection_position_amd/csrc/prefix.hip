@@ -314,21 +314,23 @@ __global__ __launch_bounds__(PCfg<D>::kThreads, PCfg<D>::kMinWaves) void prefix_
       x.m = x.lim = -INFINITY;
       x.l = x.off = 0.f;
     };
-    begin(A, row_a);
-    begin(B, row_a + 32);
     if (n > 0) {
       if (!kWide) {
 #pragma unroll 1
         for (int i = 0; i < C::S + 2; ++i) look_up(i);
+        big::wait_vmcnt<0>();
+        asm volatile("" ::: "memory");
       }
-      big::wait_vmcnt<0>();
-      asm volatile("" ::: "memory");
 #pragma unroll 1
       for (int i = 0; i < C::S; ++i) {
         const Off o = kWide ? wide_off(i) : Off{};
         load(i, kK, o);
         if (i < C::S - 1) load(i, kV, o);
       }
+    }
+    begin(A, row_a);
+    begin(B, row_a + 32);
+    if (n > 0) {
       if (!kWide) {
 #pragma unroll 1
         for (int i = C::S + 2; i < 2 * C::S; ++i) look_up(i);
