@@ -57,7 +57,14 @@ struct AttnArgs {
                    // sequences) and one for each sequence that is in one piece, of slot_rows
   float* part_ml;  // [Hkv, row tiles, 2 G, rows of a tile, 2]: maximum and sum; of an unused node's row the last piece has kUnused
   int2* pieces;    // [batch]: the first and the last part with a tile of the sequence (NULL: nothing to join)
-  // a shared prefix's pieces: [Hkv, slots, rows of a tile, D] as the prefix's own kernel leaves them, or by tree
+  int batch, T, group, G, row_tiles;
+  bool whole;  // parts are sequences
+  int spread;  // 16-lane groups that join a row's pieces: 1, 4 or 16
+  float c2;  // scale * log2(e)
+  // Of a batch with a shared prefix.
+  int cut_slots;
+  int slot_rows;  // kOwn: of a slot, as many as there are where one tile has them all
+  // the prefix's pieces: [Hkv, slots, rows of a tile, D] as the prefix's own kernel leaves them, or by tree
   // attention's [Hkv, parts, rows of the batch, D] with their count, and their maxima and sums
   float* prefix_o;
   float* prefix_ml;
@@ -67,13 +74,6 @@ struct AttnArgs {
   int prefix_most;  // the longest that its table has
   int* prefix_count;
   int prefix_G;
-  int batch, T, group, G, row_tiles;
-  int nodes;  // of a sequence that are keys: T, or none of the prefix
-  int cut_slots;
-  int slot_rows;  // kOwn: of a slot, as many as there are where one tile has them all
-  bool whole;  // parts are sequences
-  int spread;  // 16-lane groups that join a row's pieces: 1, 4 or 16
-  float c2;  // scale * log2(e)
 };
 
 // KW key groups x RW row groups of waves, a ring of S stages of 32 SUB keys; kOnce: one workgroup
@@ -116,9 +116,13 @@ __device__ __forceinline__ uint64_t shfl64(uint64_t x, int src) {
 }
 
 // Tiles of a sequence: its keys are the cache's and right behind them the tree's.
-template <class C>
+template <class C, Role kRole>
+__device__ __forceinline__ int tiles_of(const AttnArgs& a, int len) {
+  return (len + (kRole == kPrefix ? 0 : a.T) + C::kTile - 1) / C::kTile;
+}
+template <class C, Role kRole>
 __device__ __forceinline__ int seq_tiles(const AttnArgs& a, int b) {
-  return (a.c.len(b) + a.nodes + C::kTile - 1) / C::kTile;
+  return tiles_of<C, kRole>(a, a.c.len(b));
 }
 
 // Parts that `total` tiles are cut into: from 32 a sequence on of four tiles or more, as the join reads every
@@ -136,9 +140,9 @@ struct Where {
   int total, before, seq;
 };
 // Up to 64 sequences: a lane each, every wave by itself.
-template <class C, class F>
+template <class C, Role kRole, class F>
 __device__ __forceinline__ Where locate_wave(const AttnArgs& a, int lane, F want) {
-  const int mine = lane < a.batch ? seq_tiles<C>(a, lane) : 0;
+  const int mine = lane < a.batch ? seq_tiles<C, kRole>(a, lane) : 0;
   int upto = mine;  // tiles of the sequences up to this lane's
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -153,16 +157,16 @@ __device__ __forceinline__ Where locate_wave(const AttnArgs& a, int lane, F want
   return w;
 }
 // More: a run of sequences per thread; scratch: kThreads + 2 values of LDS.
-template <class C, class F>
+template <class C, Role kRole, class F>
 __device__ __forceinline__ Where locate(const AttnArgs& a, int* scratch, F want) {
-  if (a.batch == 1) return Where{seq_tiles<C>(a, 0), 0, 0};
-  if (a.batch <= 64) return locate_wave<C>(a, threadIdx.x & 63, want);
+  if (a.batch == 1) return Where{seq_tiles<C, kRole>(a, 0), 0, 0};
+  if (a.batch <= 64) return locate_wave<C, kRole>(a, threadIdx.x & 63, want);
   constexpr int kThreads = C::kThreads;
   const int per = (a.batch + kThreads - 1) / kThreads;
   const int lo = threadIdx.x * per, hi = min(lo + per, a.batch);
   int mine = 0;
 #pragma unroll 1
-  for (int b = lo; b < hi; ++b) mine += seq_tiles<C>(a, b);
+  for (int b = lo; b < hi; ++b) mine += seq_tiles<C, kRole>(a, b);
   scratch[threadIdx.x] = mine;
   __syncthreads();
   int before = 0, total = 0;
@@ -176,7 +180,7 @@ __device__ __forceinline__ Where locate(const AttnArgs& a, int* scratch, F want)
   if (x >= before && x < before + mine) {
     int b = lo, at = before;
 #pragma unroll 1
-    for (int n; x >= at + (n = seq_tiles<C>(a, b)); ++b) at += n;
+    for (int n; x >= at + (n = seq_tiles<C, kRole>(a, b)); ++b) at += n;
     scratch[kThreads] = at;
     scratch[kThreads + 1] = b;
   }
@@ -347,9 +351,9 @@ __device__ __forceinline__ void attend(const AttnArgs& a, int block, Shared<C>& 
   // part g: the tiles x .. x_end - 1, at least one
   int x = 0, x_end, seq = g, before = 0, total = 0, parts = 0;
   if (a.whole) {
-    x_end = seq_tiles<C>(a, g);
+    x_end = seq_tiles<C, kRole>(a, g);
   } else {
-    const Where w = locate<C>(a, scratch, [&](int total) {
+    const Where w = locate<C, kRole>(a, scratch, [&](int total) {
       return min(mul_div(g, total, parts_of(a, total)), total - 1);
     });
     total = uniform(w.total), parts = parts_of(a, total);
@@ -375,7 +379,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, int block, Shared<C>& 
 
   while (x < x_end) {
     const int len = a.c.len(seq);
-    const int tiles = (len + a.nodes + C::kTile - 1) / C::kTile;
+    const int tiles = tiles_of<C, kRole>(a, len);
     const int first = x - before, last = min(tiles, x_end - before);
     // for the join: tile y is in part floor(((y + 1) parts - 1) / total)
     if (a.pieces && first == 0 && head == 0 && rt == 0 && threadIdx.x == 0)
@@ -498,7 +502,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, int block, Shared<C>& 
       char* kt = const_cast<char*>(ring) + i % C::S * C::kStage;
       char* vt = kt + C::kHalf;
       const int base = (first + i) * C::kTile + kw * C::kKeys;  // first key
-      const int cached = len - base, left = cached + a.nodes;     // of the cache's, of all, from there on
+      const int cached = len - base, left = cached + (kRole == kPrefix ? 0 : a.T);  // of the cache's, of all, from there on
       const bool masked = cached < C::kKeys;
       uint64_t see = ~0ull;
       if (masked) {
@@ -874,7 +878,6 @@ AttnArgs attention_args(const AttnPlan& p, const CacheView& c, const void* q, co
   a.whole = p.whole;
   a.batch = (int)batch;
   a.T = (int)T;
-  a.nodes = (int)T;
   a.group = (int)group;
   a.G = (int)p.G;
   a.row_tiles = (int)p.row_tiles;
@@ -974,7 +977,6 @@ hipError_t launch_shared_attention(const SharedPlan& p, const CacheView& c, cons
   b.c = prefix;
   b.batch = 1;
   b.T = (int)(batch * T);
-  b.nodes = 0;
   b.G = b.prefix_G;
   b.row_tiles = (int)p.prefix_tiles;
   b.whole = false;
