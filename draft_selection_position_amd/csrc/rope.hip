@@ -10,6 +10,11 @@
 // Angles.  a / (pi / 2) = n + r, |r| <= 1/2, formed in 64 bits (two roundings: at position 2^20 and
 // frequency 1 the quarter turn is off by 2^-32).  Sine and cosine of r pi / 2 are their series in fp32
 // (the terms left out are below 2^-29 and 2^-33); n picks the quadrant.
+//
+// Bound by memory: 16320 tokens of 32 + 8 heads of 128, k and v out of their joint rows too, bf16, 401 MB read and written: 78.5 us, 5.1
+// TB/s; 65536 tokens of 16 prompts into pages of 64 with their queries, 1.6 GB: 305 us, 5.3 TB/s; 4003 x 25 heads of 80,
+// 20 of them turned, fp32: 12.8 us.  One token: 3.2 us on the device, the launch and two latencies; a block of 17 into
+// the cache: 3.9 (starts, length and page in turn).  4096 trees' positions: 3.2 us.
 #include <algorithm>
 #include <type_traits>
 

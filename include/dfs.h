@@ -528,7 +528,7 @@ int dfs_cache_append(const void* q, const void* k, const void* v, const int32_t*
  * a document, one prompt's many answers) that lies in the pool once: node t of sequence b sees the
  * prefix's positions 0 .. prefix_len - 1, its sequence's own cache, itself and its ancestors, under one
  * softmax.  The prefix's keys and values meet the query rows of the whole batch in one matrix
- * product: they are read once for all sequences (for every 128 or 256 query rows of a kv head).
+ * product: they are read once for all sequences (in tiles of up to 256 query rows of a kv head).
  *   prefix_table [prefix_width] int32: the prefix's pages, prefix_len [1] int32 (clamped to
  *   [0, prefix_width * page_size]; entries past it are not read, those that are, clamped to the pool);
  *   everything else as for dfs_tree_attention (lens and block_table are of what follows the prefix).
