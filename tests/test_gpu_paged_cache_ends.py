@@ -171,3 +171,23 @@ def test_prompts_in_pieces(dfs):
     assert torch.equal(lens, whole) and torch.equal(torch.cat(parts), q)
     assert all(torch.equal(s, t) for s, t in zip(*pools))
     assert np.isfinite(q.float().cpu().numpy()).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,T,Hkv,group,page,width,many", [
+    ([511, 0, 512, 513, 1023, 1024, 1025, 40], 1, 8, 4, 16, 0, False),  # parts of 16 tiles, and what is just too long for one
+    ([1537, 3, 2047, 0], 5, 4, 2, 64, 0, False),
+    ([2600, 0, 700, 30, 5, 1], 2, 2, 16, 1, 5000, False),               # a table for more keys than there are: parts without any
+    ([1500, 9, 500, 0], 4, 8, 1, 16, 0, True)])
+def test_own_keys_in_parts_by_single_waves(dfs, D, lens, T, Hkv, group, page, width, many):
+    n = len(lens)
+    a = make_shared(76, 200, lens, T, Hkv, group, D, page, "holes")
+    B = -(-1024 // Hkv)
+    rep = lambda t: t[torch.arange(B, device="cuda") % n].contiguous()  # noqa: E731
+    a = [randn(gen(77), B, T, Hkv * group, D, dtype=BF16), *(rep(t) for t in a[1:4]), *a[4:8], wide(rep(a[8]), width // page), rep(a[9])]
+    if many:
+        a = large(a)
+    out = dfs.tree_attention_shared(*a)
+    for lo in range(0, B, 256):
+        check(dfs, [*(t[lo:lo + 256] for t in a[:4]), *a[4:8], a[8][lo:lo + 256], a[9][lo:lo + 256]], got=out[lo:lo + 256])
+    assert torch.equal(bits(dfs.tree_attention_shared(*a)), bits(out))
