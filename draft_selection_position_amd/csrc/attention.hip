@@ -59,17 +59,16 @@ struct AttnArgs {
   const uint16_t* v_new;
   const int32_t* parents;
   uint16_t* out;
-  float* part_o;   // [Hkv, row tiles, 2 G, rows of a tile, D]; kOwn: cut_slots (2 G, or none where no sequence is
-                   // cut) and one for each sequence that is in one piece, of slot_rows
+  float* part_o;   // [Hkv, row tiles, 2 G, rows of a tile, D]; kOwn: cut_slots (2 G, or none of parts that are
+                   // sequences) and one for each sequence that is in one piece, of slot_rows
   float* part_ml;  // [Hkv, row tiles, 2 G, rows of a tile, 2]: maximum and sum; of an unused node's row the last piece has kUnused
   int2* pieces;    // [batch]: the first and the last part with a tile of the sequence (NULL: nothing to join)
   int batch, T, group, G, row_tiles;
-  bool whole;  // parts are sequences, or (kOwn) parts of one
+  bool whole;  // parts are sequences
   int spread;  // 16-lane groups that join a row's pieces: 1, 4 or 16
   float c2;  // scale * log2(e)
   // Of a batch with a shared prefix.
   int cut_slots;
-  int split, chunk;  // kOwn, `whole`: parts of a sequence, and tiles of one, at most
   int slot_rows;  // kOwn: of a slot, as many as there are where one tile has them all
   // the prefix's pieces: [Hkv, slots, rows of a tile, D] as the prefix's own kernel leaves them, or by tree
   // attention's [Hkv, parts, rows of the batch, D] with their count, and their maxima and sums
@@ -354,21 +353,11 @@ __device__ __forceinline__ void attend(const AttnArgs& a, int block, Shared<C>& 
   const int turn = block / (8 * a.row_tiles), rt = block / 8 % a.row_tiles;
   const int unit = turn * 8 + block % 8;  // (head, part)
   if (unit >= Hkv * a.G) return;
-  const int head = unit / a.G;
-  int g = unit % a.G;
+  const int head = unit / a.G, g = unit % a.G;
   // part g: the tiles x .. x_end - 1, at least one
   int x = 0, x_end, seq = g, before = 0, total = 0, parts = 0;
   if (a.whole) {
-    if constexpr (kRole == kOwn) {
-      const int p = g / a.batch;  // all first parts, all second ones: XCDs get the same of each
-      seq = g % a.batch;
-      g = seq * a.split + p;
-      const int tiles = seq_tiles<C, kRole>(a, seq), n = (tiles + a.chunk - 1) / a.chunk;
-      if (p >= n) return;
-      x = (int)((int64_t)p * tiles / n), x_end = (int)((int64_t)(p + 1) * tiles / n);
-    } else {
-      x_end = seq_tiles<C, kRole>(a, g);
-    }
+    x_end = seq_tiles<C, kRole>(a, g);
   } else {
     const Where w = locate<C, kRole>(a, scratch, [&](int total) {
       return min(mul_div(g, total, parts_of(a, total)), total - 1);
@@ -400,9 +389,8 @@ __device__ __forceinline__ void attend(const AttnArgs& a, int block, Shared<C>& 
     const int first = x - before, last = min(tiles, x_end - before);
     // for the join: tile y is in part floor(((y + 1) parts - 1) / total)
     if (a.pieces && first == 0 && head == 0 && rt == 0 && threadIdx.x == 0)
-      a.pieces[seq] = make_int2(g, kRole == kOwn && a.whole
-                                       ? g + (tiles + a.chunk - 1) / a.chunk - 1
-                                       : (int)(((double)(before + tiles) * (double)parts - 1.0) / (double)total));
+      a.pieces[seq] = make_int2(
+          g, kRole == kOwn && a.whole ? g : (int)(((double)(before + tiles) * (double)parts - 1.0) / (double)total));
     const int n = last - first;  // steps
     // nothing cached: no entry of the table counts, and look-ups read the length (unused) in its place
     const int32_t* table = len > 0 ? a.c.block_table + (int64_t)seq * a.c.table_width : a.c.lens + seq;
@@ -835,21 +823,10 @@ bool prefix_is_large(int64_t rows, int64_t kv_heads, int64_t D, int64_t longest)
 // keys the saved launch pays (16 tokens x 8 heads x 4 of 128, 4001 keys, own 77: 21.2 us against 29.5, 4000: 48 and 51, 8000: 75
 // and 71, 16000: 121 and 107; 40 tokens x 2 x 4 of 64, 8000: 32 and 36, 16000: 50 and 46).
 constexpr int64_t kBesideKeys = 8192;
-// Otherwise, up to 32 rows of a sequence and head, and 1024 of these or more (512, where they may be long but need no
-// launch of their own): a wave for each, four or more of them on a CU, where a workgroup that goes through several in turn
-// waits for each one's start, and where the tiles of `beside` are those of the whole batch.  Long ones are cut, so that
-// the waves end together.  One token, 4 heads to a kv head of 128 (us a call, against the other ways): 256 x 8 kv heads, up to 100 own
-// keys 64 and 96, up to 1024 181 (uncut 189) and 206, 9000 794 and 836; 128 x 8, 8000 424 and 481; 64 x 8, 2000 86 and 96,
-// 1000 57 both, 500 55 and 42.  8 heads of 64: 1024 x 1, 12000 312 and 433.  At worst 128 x 8, 15000 697 and 670; 64 x 8, 100 keys in a
-// table for 4000 40 and 35.
-constexpr int64_t kLongByWaves = 16384;
-bool own_by_waves(int64_t rows, int64_t pairs, int64_t longest) {
-  return rows <= 32 && (pairs >= 1024 ? longest <= kLongByWaves : pairs >= 512 && longest >= 2048 && longest <= kBesideKeys);
-}
-// Tiles of a wave's part at most: 16, or more where full tables would make more than 8192 parts (16384 parts: 397 -> 437 us at 64
-// x 16 heads, 7900 keys; 16 tiles against 8: 189 and 193 at 256 x 8, 1024 keys).
-int64_t wave_tiles(int64_t each, int64_t pairs) { return std::min(each, std::max<int64_t>(16, each * pairs / 8192)); }
-
+// Otherwise, up to 32 rows of a sequence and head, 1024 of these or more and no long one: a wave for each, four or
+// more of them on a CU, where a workgroup that goes through several in turn waits for each one's start (256 tokens x 8 x 4 of 128,
+// up to 100 own keys: 64 us a call against 96, up to 1024: 194 and 206; 256 x 4 x 8, up to 2000: 145 both).
+bool own_by_waves(int64_t rows, int64_t pairs, int64_t longest) { return rows <= 32 && pairs >= 1024 && longest <= 2048; }
 
 template <int D, class F>
 auto with_own_cfg(int64_t rows, bool single, F f) {
@@ -874,9 +851,7 @@ AttnPlan plan_attention(const CacheView& c, int64_t batch, int64_t T, int64_t gr
     // against 10.2; 39 x 33 nodes, up to 61 keys: 17.8 against 24.4; 13 x 56 nodes, 7 heads, 243 keys: 16.2
     // against 27.9; at worst 2 x 18 nodes, 3 heads, 115 keys: 14.0 against 12.8).
     p.whole = whole || each <= 4 || (each <= 8 && batch * c.kv_heads * p.row_tiles >= 48);
-    p.chunk = whole ? wave_tiles(each, batch * c.kv_heads) : each;
-    p.split = cdiv(each, p.chunk);
-    if (p.whole) p.G = batch * p.split;
+    if (p.whole) p.G = batch;
     p.tile_rows = C::kRows;
     const int64_t rows = (int64_t)c.kv_heads * p.row_tiles * 2 * p.G * C::kRows;
     const bool join = p.G > 1 && !p.whole;
@@ -963,7 +938,7 @@ SharedPlan plan_shared_attention(const CacheView& c, const CacheView& prefix, in
     rows = c.kv_heads * p.prefix_parts * all_rows;
     p.count = take(4);
   }
-  p.cut_slots = p.own.whole && p.own.split == 1 ? 0 : 2 * p.own.G;
+  p.cut_slots = p.own.whole ? 0 : 2 * p.own.G;
   p.slot_rows = p.own.row_tiles == 1 ? T * group : p.own.tile_rows;
   const int64_t own_rows = c.kv_heads * p.own.row_tiles * (p.cut_slots + batch) * p.slot_rows;
   p.own_o = take((size_t)(own_rows * D) * 4);
@@ -993,8 +968,6 @@ hipError_t launch_shared_attention(const SharedPlan& p, const CacheView& c, cons
   a.prefix_G = (int)p.prefix_parts;
   a.cut_slots = (int)p.cut_slots;
   a.slot_rows = (int)p.slot_rows;
-  a.split = (int)p.own.split;
-  a.chunk = (int)p.own.chunk;
   const int64_t pieces = p.prefix_parts + cdiv(p.own.G, batch);
   // by a row's pieces, but no more workgroups than help (16 rows x 8 heads, 28 pieces: 14.2 us a call by 16 against 16.5 by 4;
   // 128 x 8 x 4 rows, 17 pieces: 96 by 4 against 107)

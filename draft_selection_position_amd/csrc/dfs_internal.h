@@ -249,8 +249,7 @@ struct AttnPlan {
   int64_t G;               // parts that the keys of a head are cut into
   int64_t slots;           // workgroups that the card holds at once
   int64_t tile_rows;       // of a row tile
-  bool whole;              // parts are sequences: nothing to join; of own keys beside a shared prefix also
-  int64_t split, chunk;    // up to `split` parts of a sequence, of up to `chunk` tiles
+  bool whole;              // parts are sequences: nothing to join
   size_t part_bytes;       // of the parts' fp32 sums,
   size_t ml_bytes;         // of their maxima and sums; each sequence's parts follow
   size_t ws_bytes;

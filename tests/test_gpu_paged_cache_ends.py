@@ -175,11 +175,11 @@ def test_prompts_in_pieces(dfs):
 
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("lens,T,Hkv,group,page,width,many", [
-    ([511, 0, 512, 513, 1023, 1024, 1025, 40], 1, 8, 4, 16, 0, False),  # parts of 16 tiles, and what is just too long for one
+    ([511, 0, 512, 513, 1023, 1024, 1025, 40], 1, 8, 4, 16, 0, False),
     ([1537, 3, 2047, 0], 5, 4, 2, 64, 0, False),
-    ([2600, 0, 700, 30, 5, 1], 2, 2, 16, 1, 5000, False),               # a table for more keys than there are: parts without any
+    ([2600, 0, 700, 30, 5, 1], 2, 2, 16, 1, 5000, False),               # a table for more keys than there are
     ([1500, 9, 500, 0], 4, 8, 1, 16, 0, True)])
-def test_own_keys_in_parts_by_single_waves(dfs, D, lens, T, Hkv, group, page, width, many):
+def test_own_keys_of_many_sequences(dfs, D, lens, T, Hkv, group, page, width, many):
     n = len(lens)
     a = make_shared(76, 200, lens, T, Hkv, group, D, page, "holes")
     B = -(-1024 // Hkv)
