@@ -824,9 +824,14 @@ bool prefix_is_large(int64_t rows, int64_t kv_heads, int64_t D, int64_t longest)
 // and 71, 16000: 121 and 107; 40 tokens x 2 x 4 of 64, 8000: 32 and 36, 16000: 50 and 46).
 constexpr int64_t kBesideKeys = 8192;
 // Otherwise, up to 32 rows of a sequence and head, 1024 of these or more and no long one: a wave for each, four or
-// more of them on a CU, where a workgroup that goes through several in turn waits for each one's start (256 tokens x 8 x 4 of 128,
-// up to 100 own keys: 64 us a call against 96, up to 1024: 194 and 206; 256 x 4 x 8, up to 2000: 145 both).
-bool own_by_waves(int64_t rows, int64_t pairs, int64_t longest) { return rows <= 32 && pairs >= 1024 && longest <= 2048; }
+// more of them on a CU, where a workgroup that goes through several in turn waits for each one's start.  The last wave to
+// start may have the longest sequence: the more of them, the longer they may be.  (us a call, lengths in mixed order, against the
+// other ways; 4 heads to a kv head: 256 tokens x 8 kv heads of 128, up to 100 own keys 108 and 139, 1024 189 and 202; 256 x 4, 8 heads
+// to each, 2000 187 both; 512 x 8 of 64, 1000 161 and 187, 4000 427 and 435, 7000 768 and 752; 1024 x 8 of 64, 3000 592 and 645, 7000
+// 1278 and 1390; 2048 x 8 of 64, 12000 4159 and 4032; 256 x 8 of 128, 4000 422 and 420.)
+bool own_by_waves(int64_t rows, int64_t pairs, int64_t longest) {
+  return rows <= 32 && pairs >= 1024 && longest <= std::clamp<int64_t>(pairs, 2048, 8192);
+}
 
 template <int D, class F>
 auto with_own_cfg(int64_t rows, bool single, F f) {
