@@ -806,10 +806,6 @@ auto with_cfg(int64_t rows, F f) {
   return f(Cfg<D, 1, 4, 2, 2, false>{});
 }
 
-}  // namespace
-
-namespace {
-
 // How a batch goes over its shared prefix.  Few rows or few products: tree attention's kernel, in one launch with the
 // sequences' own keys, so that the call is two launches.  From 3 x 2^32 products of a kind on (rows x heads x the
 // prefix's longest x D), and more than 384 rows: the prefix's own kernel, which is half as fast again but fills
@@ -820,9 +816,11 @@ bool prefix_is_large(int64_t rows, int64_t kv_heads, int64_t D, int64_t longest)
   return rows > 384 && (double)rows * (double)kv_heads * (double)D * (double)longest >= 3.0 * 4294967296.0;
 }
 // In one launch the own keys go by the rows of the whole batch, in tiles that one sequence's rows do not fill: up to so many
-// keys the saved launch pays (16 tokens x 8 heads x 4 of 128, 4001 keys, own 77: 21.2 us against 29.5, 4000: 48 and 51, 8000: 75
-// and 71, 16000: 121 and 107; 40 tokens x 2 x 4 of 64, 8000: 32 and 36, 16000: 50 and 46).
-constexpr int64_t kBesideKeys = 8192;
+// keys of a sequence, and of all sequences and heads, the saved launch pays (us, lengths in mixed order; 4 heads to a kv head of 128: 16
+// tokens x 8 kv heads, up to 4000 own keys 46 and 49, 8000 67 and 65, 16000 121 and 107; 64 x 8, 1500 60 and 71, 3000 104 and 100,
+// 8000 224 and 193; 128 x 8, 8000 418 and 362; 20 x 17 nodes x 8, 3000 57 and 70; of 64: 100 x 5 x 4, 3000 66 and 70, 256 x 1
+// x 4 of 8, 5000 167 and 147, 30 x 9 x 4, 5000 38 and 52).
+bool beside_prefix(int64_t pairs, int64_t longest) { return longest <= 8192 && pairs * longest <= 5 << 18; }
 // Otherwise, up to 32 rows of a sequence and head, 1024 of these or more and no long one: a wave for each, four or
 // more of them on a CU, where a workgroup that goes through several in turn waits for each one's start.  The last wave to
 // start may have the longest sequence: the more of them, the longer they may be.  (us a call, lengths in mixed order, against the
@@ -924,7 +922,7 @@ SharedPlan plan_shared_attention(const CacheView& c, const CacheView& prefix, in
   const int64_t longest = (int64_t)c.table_width << c.page_shift, prefix_longest = (int64_t)prefix.table_width << prefix.page_shift;
   p.large = prefix_is_large(all_rows, c.kv_heads, D, prefix_longest);
   p.single = own_by_waves(T * group, batch * c.kv_heads, longest);
-  p.beside = !p.large && !p.single && longest <= kBesideKeys;
+  p.beside = !p.large && !p.single && beside_prefix(batch * c.kv_heads, longest);
   p.cfg_rows = p.beside ? all_rows : T * group;
   p.own = plan_attention(c, batch, T, group, D, p.single, [&](auto plan) {
     return D == 64 ? with_own_cfg<64>(p.cfg_rows, p.single, plan) : with_own_cfg<128>(p.cfg_rows, p.single, plan);
