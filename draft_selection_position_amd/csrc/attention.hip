@@ -821,15 +821,13 @@ bool prefix_is_large(int64_t rows, int64_t kv_heads, int64_t D, int64_t longest)
 // 8000 224 and 193; 128 x 8, 8000 418 and 362; 20 x 17 nodes x 8, 3000 57 and 70; of 64: 100 x 5 x 4, 3000 66 and 70, 256 x 1
 // x 4 of 8, 5000 167 and 147, 30 x 9 x 4, 5000 38 and 52).
 bool beside_prefix(int64_t pairs, int64_t longest) { return longest <= 8192 && pairs * longest <= 5 << 18; }
-// Otherwise, up to 32 rows of a sequence and head, 1024 of these or more and no long one: a wave for each, four or
-// more of them on a CU, where a workgroup that goes through several in turn waits for each one's start.  The last wave to
-// start may have the longest sequence: the more of them, the longer they may be.  (us a call, lengths in mixed order, against the
-// other ways; 4 heads to a kv head: 256 tokens x 8 kv heads of 128, up to 100 own keys 108 and 139, 1024 189 and 202; 256 x 4, 8 heads
-// to each, 2000 187 both; 512 x 8 of 64, 1000 161 and 187, 4000 427 and 435, 7000 768 and 752; 1024 x 8 of 64, 3000 592 and 645, 7000
-// 1278 and 1390; 2048 x 8 of 64, 12000 4159 and 4032; 256 x 8 of 128, 4000 422 and 420.)
-bool own_by_waves(int64_t rows, int64_t pairs, int64_t longest) {
-  return rows <= 32 && pairs >= 1024 && longest <= std::clamp<int64_t>(pairs, 2048, 8192);
-}
+// Up to 32 rows of a sequence and head, 1024 of these or more and no long one: a wave for each, four or more of them on a
+// CU, where a workgroup that goes through several in turn waits for each one's start.  Behind long ones the last wave ends
+// late.  (us a call, lengths in mixed order, against a launch of their own or the prefix's; 4 heads to a kv head: 256 tokens x 8 kv
+// heads of 128, up to 100 own keys 108 and 139, 1024 191 and 204; 128 x 8, 1000 94 and 99, 2000 145 and 143, 4000 237 and 206;
+// 200 x 8 nodes x 8, 1500 239 and 245; of 64: 512 x 8, 1000 161 and 192, 2000 243 and 234, 4000 440 and 384; 200 x 5 nodes x 6,
+// 1500 93 and 107.)
+bool own_by_waves(int64_t rows, int64_t pairs, int64_t longest) { return rows <= 32 && pairs >= 1024 && longest <= 1536; }
 
 template <int D, class F>
 auto with_own_cfg(int64_t rows, bool single, F f) {

@@ -214,7 +214,7 @@ def test_large_lengths_and_pages_out_of_range(dfs):
     (100, [(7 * b) % 90 for b in range(600)], 1, 2, 4, 16, 0, "chain"),         # a wave each: 1200 of them
     (0, [0] * 1024, 2, 1, 1, 16, 0, "random"),
     (1, [1] * 300, 8, 4, 4, 16, 0, "holes"),                                    # 32 rows each
-    (333, [2000, 1, 0] * 350, 3, 1, 2, 1, 0, "random"),                         # own keys up to a wave's longest
+    (333, [2000, 1, 0] * 350, 3, 1, 2, 1, 0, "random"),                         # longer own keys than a wave takes
     (333, [70, 1, 0] * 350, 3, 1, 2, 16, 200, "random"),                        # too wide a table for that
     (500, [600, 0, 33], 2, 2, 4, 16, 600, "random"),                            # own keys in a launch of their own
     (500, [900, 5], 20, 1, 2, 16, 600, "holes"),
