@@ -49,8 +49,9 @@ constexpr float kUnused = -1.0f;  // for a sum of weights
 
 // What a workgroup's keys are.  kTree: a sequence's cache and tree, the whole answer.  Of a batch with a shared prefix:
 // kOwn the same, but a piece of the answer, to be joined with the prefix's; kPrefix the prefix, for the rows of the whole
-// batch as the one sequence that it is (no node is a key then, and every row sees all).
-enum Role { kTree, kOwn, kPrefix };
+// batch as the one sequence that it is (no node is a key then, and every row sees all); kBoth, of short ones, the prefix's and
+// right behind them the sequence's, the whole answer.
+enum Role { kTree, kOwn, kPrefix, kBoth };
 
 struct AttnArgs {
   CacheView c;
@@ -76,6 +77,7 @@ struct AttnArgs {
   float* prefix_ml;
   bool large;
   PrefixCut cut;
+  const int32_t* prefix_table;
   const int32_t* prefix_len;
   int prefix_most;  // the longest that its table has
   int* prefix_count;
@@ -121,6 +123,11 @@ __device__ __forceinline__ uint64_t shfl64(uint64_t x, int src) {
   return ((uint64_t)(uint32_t)__shfl((uint32_t)(x >> 32), src) << 32) | (uint32_t)__shfl((uint32_t)x, src);
 }
 
+// The prefix's length, where its keys are in front of a sequence's own.
+template <Role kRole>
+__device__ __forceinline__ int in_front(const AttnArgs& a) {
+  return kRole == kBoth ? min(max(*a.prefix_len, 0), a.prefix_most) : 0;
+}
 // Tiles of a sequence: its keys are the cache's and right behind them the tree's.
 template <class C, Role kRole>
 __device__ __forceinline__ int tiles_of(const AttnArgs& a, int len) {
@@ -128,7 +135,7 @@ __device__ __forceinline__ int tiles_of(const AttnArgs& a, int len) {
 }
 template <class C, Role kRole>
 __device__ __forceinline__ int seq_tiles(const AttnArgs& a, int b) {
-  return tiles_of<C, kRole>(a, a.c.len(b));
+  return tiles_of<C, kRole>(a, in_front<kRole>(a) + a.c.len(b));
 }
 
 // Parts that `total` tiles are cut into: from 32 a sequence on of four tiles or more, as the join reads every
@@ -384,7 +391,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, int block, Shared<C>& 
   const int64_t page_bytes = ((int64_t)Hkv << a.c.page_shift) * C::kRowBytes;
 
   while (x < x_end) {
-    const int len = a.c.len(seq);
+    const int front = in_front<kRole>(a), own = a.c.len(seq), len = front + own;
     const int tiles = tiles_of<C, kRole>(a, len);
     const int first = x - before, last = min(tiles, x_end - before);
     // for the join: tile y is in part floor(((y + 1) parts - 1) / total)
@@ -393,9 +400,9 @@ __device__ __forceinline__ void attend(const AttnArgs& a, int block, Shared<C>& 
           g, kRole == kOwn && a.whole ? g : (int)(((double)(before + tiles) * (double)parts - 1.0) / (double)total));
     const int n = last - first;  // steps
     // nothing cached: no entry of the table counts, and look-ups read the length (unused) in its place
-    const int32_t* table = len > 0 ? a.c.block_table + (int64_t)seq * a.c.table_width : a.c.lens + seq;
+    const int32_t* table = own > 0 ? a.c.block_table + (int64_t)seq * a.c.table_width : a.c.lens + seq;
     // Pages of a step's keys or more: they lie in one, read by a scalar load a step ahead.
-    const bool wide = (1 << a.c.page_shift) >= C::kKeys;
+    const bool wide = kRole != kBoth && (1 << a.c.page_shift) >= C::kKeys;
     auto wide_page = [&](int i) {
       typedef const __attribute__((address_space(4))) int32_t* const_ptr;
       const int key = min((first + i) * C::kTile + kw * C::kKeys, len - 1);
@@ -404,7 +411,8 @@ __device__ __forceinline__ void attend(const AttnArgs& a, int block, Shared<C>& 
     // Smaller ones: the pages of step i's keys, into its slot of this wave's ring.
     auto look_up = [&](int i) {
       const int key = min((first + i) * C::kTile + kw * C::kKeys + (lane & (C::kKeys - 1)), len - 1);
-      dma4(table + (max(key, 0) >> a.c.page_shift),
+      const bool of_front = kRole == kBoth && key < front;
+      dma4((of_front ? a.prefix_table : table) + (max(of_front ? key : key - front, 0) >> a.c.page_shift),
            __builtin_amdgcn_readfirstlane(pages0 + i % (C::kAhead + 1) * C::kPages));
     };
     // This wave's share of step i's K and V rows.
@@ -416,6 +424,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, int block, Shared<C>& 
       const char* kp = static_cast<const char*>(a.c.k_pages);
       const char* vp = static_cast<const char*>(a.c.v_pages);
       const int in_page = (1 << a.c.page_shift) - 1;
+      auto place = [&](int key) { return key < front ? key : key - front; };
       if (base + C::kKeys > len) {  // nodes among them, or nothing
 #pragma unroll
         for (int u = 0; u < C::kLoads; ++u) {
@@ -424,7 +433,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, int block, Shared<C>& 
           const int row = j * C::kRowsPerLoad + rr, key = kRole == kPrefix ? min(base + row, len - 1) : base + row;
           const int page = min(max(wide ? wide_id : pages[row], 0), a.c.n_pages - 1);
           const int64_t cached = (int64_t)page * page_bytes +
-                                 (int64_t)((head << a.c.page_shift) + (key & in_page)) * C::kRowBytes;
+                                 (int64_t)((head << a.c.page_shift) + (place(key) & in_page)) * C::kRowBytes;
           const int64_t node = (((int64_t)seq * a.T + min(key - len, a.T - 1)) * Hkv + head) * C::kRowBytes;
           const bool tree = kRole != kPrefix && key >= len;
           dma16<C::kOnce>((tree ? reinterpret_cast<const char*>(a.k_new) + node : kp + cached) + 16 * k_slot<C>(slot, row),
@@ -456,7 +465,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, int block, Shared<C>& 
         const int row = j * C::kRowsPerLoad + rr;
         const int page = min(max(pages[row], 0), a.c.n_pages - 1);
         const int64_t off = (int64_t)page * page_bytes +
-                            (int64_t)((head << a.c.page_shift) + ((base + row) & in_page)) * C::kRowBytes;
+                            (int64_t)((head << a.c.page_shift) + (place(base + row) & in_page)) * C::kRowBytes;
         dma16<C::kOnce>(kp + off + 16 * k_slot<C>(slot, row), __builtin_amdgcn_readfirstlane(to + j * 1024));
         dma16<C::kOnce>(vp + off + 16 * v_slot<C>(slot, row), __builtin_amdgcn_readfirstlane(to + C::kHalf + j * 1024));
       }
@@ -548,7 +557,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, int block, Shared<C>& 
     // A lane's values in fours, d = 4 h + 8 u of its row.  Key groups: joined through LDS, a
     // share of the fours to each wave (one wave for all of them: 1.8 us against 1.1 for a
     // single token).
-    const bool whole = kRole == kTree && first == 0 && last == tiles;
+    const bool whole = (kRole == kTree || kRole == kBoth) && first == 0 && last == tiles;
     constexpr int kFours = C::D / 8, kMine = kFours / C::KW;
     float m = st.m, l = st.l + xor32(st.l, lane);
     f32x4 o[kMine];
@@ -829,6 +838,16 @@ bool beside_prefix(int64_t pairs, int64_t longest) { return longest <= 8192 && p
 // 1500 93 and 107.)
 bool own_by_waves(int64_t rows, int64_t pairs, int64_t longest) { return rows <= 32 && pairs >= 1024 && longest <= 1536; }
 
+// Few keys in all, by the tables' widths: a workgroup takes the prefix's and a sequence's own, in one launch and without
+// pieces, although every sequence reads the prefix again (us, against the other ways; heads of 128, 4 to each of 8 kv heads: 64 x 17
+// nodes, prefix 100, up to 50 own keys 20 and 35, 550 and 50 35 and 44, 900 and 50 49 and 50; 32 tokens, 300 and 100 14 and 18, 4
+// tokens 14.0 and 13.1 but a launch less for the host, 8 tokens, 900 and 50 20 and 13; 256 tokens, 100 and 100 70 and 44; 183 x 26 nodes, 7
+// x 2, 2 and 65 40 and 62; 107 x 23, 4 x 7 of 64, 600 43 and 56).
+bool few_keys(int64_t rows, int64_t pairs, int64_t longest) {
+  if (rows <= 32) return longest <= 512 && pairs <= 512;
+  return longest <= 256 || (longest <= 768 && pairs * cdiv(rows, 128) >= 48);
+}
+
 template <int D, class F>
 auto with_own_cfg(int64_t rows, bool single, F f) {
   if (single) return f(Cfg<D, 1, 1, 2, 1>{});
@@ -918,6 +937,14 @@ SharedPlan plan_shared_attention(const CacheView& c, const CacheView& prefix, in
   };
   int64_t rows;
   const int64_t longest = (int64_t)c.table_width << c.page_shift, prefix_longest = (int64_t)prefix.table_width << prefix.page_shift;
+  p.both = few_keys(T * group, batch * c.kv_heads, prefix_longest + longest + T);
+  if (p.both) {
+    p.own = plan_attention(c, batch, T, group, D, true, [&](auto plan) {
+      return D == 64 ? with_cfg<64>(T * group, plan) : with_cfg<128>(T * group, plan);
+    });
+    p.ws_bytes = 256;
+    return p;
+  }
   p.large = prefix_is_large(all_rows, c.kv_heads, D, prefix_longest);
   p.single = own_by_waves(T * group, batch * c.kv_heads, longest);
   p.beside = !p.large && !p.single && beside_prefix(batch * c.kv_heads, longest);
@@ -969,6 +996,12 @@ hipError_t launch_shared_attention(const SharedPlan& p, const CacheView& c, cons
   a.prefix_G = (int)p.prefix_parts;
   a.cut_slots = (int)p.cut_slots;
   a.slot_rows = (int)p.slot_rows;
+  if (p.both) {
+    a.prefix_table = prefix.block_table;
+    a.pieces = nullptr;
+    auto run = [&](auto cfg) { return launch<decltype(cfg), kBoth>(a, stream); };
+    return D == 64 ? with_cfg<64>(T * group, run) : with_cfg<128>(T * group, run);
+  }
   const int64_t pieces = p.prefix_parts + cdiv(p.own.G, batch);
   // by a row's pieces, but no more workgroups than help (16 rows x 8 heads, 28 pieces: 14.2 us a call by 16 against 16.5 by 4;
   // 128 x 8 x 4 rows, 17 pieces: 96 by 4 against 107)

@@ -270,6 +270,7 @@ hipError_t launch_prefix_attention(const CacheView& prefix, const PrefixCut& cut
 // The same over a prefix that the batch shares, `prefix` being its one-sequence cache.
 struct SharedPlan {
   AttnPlan own;          // of the sequences' own keys
+  bool both;             // few keys of either: one launch, without pieces; otherwise
   bool large;            // the batch has rows enough for the prefix's own kernel,
   PrefixCut cut;         // with its cut,
   bool single;           // and sequences enough for a wave each; otherwise tree attention's kernel takes the prefix:

@@ -6,7 +6,7 @@ import torch
 
 from oracle import paged_cache as pc
 
-from .test_gpu_paged_cache import BF16, F32, check_rotated, frequencies, i32, make_shared
+from .test_gpu_paged_cache import BF16, F32, SHARED, check_rotated, frequencies, i32, make_shared
 from .test_gpu_shared_prefix import ancestors_mask, check, large, wide
 from .test_gpu_target_pass import dfs, gen, randn, trees  # noqa: F401
 
@@ -191,3 +191,40 @@ def test_own_keys_of_many_sequences(dfs, D, lens, T, Hkv, group, page, width, ma
     for lo in range(0, B, 256):
         check(dfs, [*(t[lo:lo + 256] for t in a[:4]), *a[4:8], a[8][lo:lo + 256], a[9][lo:lo + 256]], got=out[lo:lo + 256])
     assert torch.equal(bits(dfs.tree_attention_shared(*a)), bits(out))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("prefix,lens,T,Hkv,group,page,kind", [
+    (0, [0, 0], 1, 1, 1, 1, "chain"), (1, [0, 5], 1, 3, 4, 1, "chain"), (127, [0, 1, 70], 5, 2, 4, 16, "holes"),  # up to 32 rows
+    (128, [200, 0], 8, 2, 4, 32, "random"), (300, [77, 31, 33], 3, 1, 8, 64, "holes"),
+    (2, [65, 0, 40], 26, 3, 2, 1, "chain"), (33, [0, 31, 64], 20, 2, 3, 8, "holes"), (64, [64, 1], 64, 1, 1, 64, "random"),  # up to 64
+    (97, [30, 3], 24, 1, 4, 16, "random"), (1, [100] * 5, 33, 2, 3, 4, "holes"), (90, [50, 0], 64, 2, 5, 32, "random"),     # more
+    (400, [100, 7, 0, 250] * 10, 17, 2, 4, 16, "holes"), (500, [0] * 30, 40, 2, 1, 128, "random"), (255, [300, 9] * 30, 20, 1, 2, 2, "holes")])
+def test_few_keys_in_one_launch(dfs, D, prefix, lens, T, Hkv, group, page, kind):
+    a = make_shared(prefix + T, prefix, lens, T, Hkv, group, D, page, kind)
+    for n in sorted({prefix, prefix // 2, 0, min(prefix, 1)}):
+        a[7] = i32([n])
+        check(dfs, a)
+    a[7] = i32([prefix])
+    clean = dfs.tree_attention_shared(*a)
+    # behind the prefix's end and the sequences' ends, and on pages of nobody, anything may lie
+    b = make_shared(prefix + T, prefix, lens, T, Hkv, group, D, page, kind, fill=float("nan"))
+    check(dfs, b)
+    assert torch.equal(bits(dfs.tree_attention_shared(*a)), bits(clean))
+    if prefix > 11:  # seen by all rows but those of unused nodes
+        used = ancestors_mask(a[3]).any(dim=2)
+        a[5][a[6][11 // page].long(), 0, 11 % page, 5] = float("inf")
+        got = dfs.tree_attention_shared(*a)
+        assert not torch.isfinite(got[used][:, :group, 5].float()).any() and torch.isfinite(got[used][..., 6:].float()).all()
+        assert (got[~used] == 0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("prefix,lens,T,Hkv,group,page,kind", SHARED)
+def test_few_keys_in_wide_tables(dfs, D, prefix, lens, T, Hkv, group, page, kind):
+    """What goes by the tables' widths goes another way."""
+    a = make_shared(prefix + T, prefix, lens, T, Hkv, group, D, page, kind)
+    a[6] = wide(a[6], 2000 // page + 1)
+    check(dfs, a)
+    a[8] = wide(a[8], 9000 // page)
+    check(dfs, a)
