@@ -528,12 +528,15 @@ int dfs_cache_append(const void* q, const void* k, const void* v, const int32_t*
  * a document, one prompt's many answers) that lies in the pool once: node t of sequence b sees the
  * prefix's positions 0 .. prefix_len - 1, its sequence's own cache, itself and its ancestors, under one
  * softmax.  The prefix's keys and values meet the query rows of the whole batch in one matrix
- * product: they are read once for all sequences (in tiles of up to 256 query rows of a kv head).
+ * product: they are read once for all sequences (in tiles of up to 256 query rows of a kv head),
+ * unless there are only a few keys in all.
  *   prefix_table [prefix_width] int32: the prefix's pages, prefix_len [1] int32 (clamped to
  *   [0, prefix_width * page_size]; entries past it are not read, those that are, clamped to the pool);
  *   everything else as for dfs_tree_attention (lens and block_table are of what follows the prefix).
  * 1 <= prefix_width, prefix_width * page_size <= 2^30; out does not overlap the prefix's arrays either.
- * ws: dfs_tree_attention_shared_workspace_bytes(shape, prefix_width) bytes of scratch (never 0). */
+ * ws: dfs_tree_attention_shared_workspace_bytes(shape, prefix_width) bytes of scratch (never 0).
+ * The order of sums goes by the sizes, the tables' widths among them, and by the lengths: equal
+ * calls give equal bits. */
 size_t dfs_tree_attention_shared_workspace_bytes(const dfs_cache_shape_t* shape, int64_t prefix_width);
 int dfs_tree_attention_shared(const void* q, const void* k_new, const void* v_new, const int32_t* parents,
                               const void* k_pages, const void* v_pages, const int32_t* prefix_table,
