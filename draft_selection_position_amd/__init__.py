@@ -808,10 +808,11 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
     """(freqs fp32 [rot_dim / 2], amplitude) of a model's rotary positions (see dfs_rope_frequencies), for ``rope``.
 
     ``scaling`` None, "linear", "ntk", "yarn" or "bands"; ``original``: the positions that the model was trained
-    on, for the last two ("bands": beta_fast and beta_slow are its high and low frequency factors)."""
+    on, for the last two ("bands": beta_fast and beta_slow are its high and low frequency factors).  ``device``:
+    where freqs goes; without one it stays on the host."""
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling must be one of {list(_SCALINGS)}, got {scaling!r}")
-    freqs = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.float32)
+    freqs = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.float32, device="cpu")  # whatever the default device is
     amplitude = ctypes.c_double()
     _check(lib().dfs_rope_frequencies(rot_dim, base, _SCALINGS[scaling], factor, original, beta_fast, beta_slow,
                                       freqs.data_ptr(), ctypes.byref(amplitude)), "dfs_rope_frequencies")

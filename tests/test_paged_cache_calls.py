@@ -1,0 +1,19 @@
+"""Calls of the operators around a paged cache that differ from the usual ones in what surrounds them (CPU)."""
+import pytest
+import torch
+
+import draft_selection_position_amd as dfs
+
+from .test_target_pass_oracle import L  # noqa: F401
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(scaling="yarn", factor=8.0, original=4096.0)])
+def test_frequencies_under_another_default_device(L, kw):  # noqa: F811
+    """They are computed on the host, whatever device a program builds its model on."""
+    want, amplitude = dfs.rope_frequencies(64, 10000.0, **kw)
+    with torch.device("meta"):
+        got, same = dfs.rope_frequencies(64, 10000.0, **kw)
+        moved, _ = dfs.rope_frequencies(64, 10000.0, **kw, device="cpu")
+        away, _ = dfs.rope_frequencies(64, 10000.0, **kw, device="meta")
+    assert got.device.type == "cpu" and torch.equal(got, want) and same == amplitude
+    assert torch.equal(moved, want) and away.device.type == "meta" and away.shape == want.shape
