@@ -812,6 +812,8 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
     where freqs goes; without one it stays on the host."""
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling must be one of {list(_SCALINGS)}, got {scaling!r}")
+    if not 0 <= rot_dim <= 1024:
+        rot_dim = 0  # refused as any other that no head has, but held by the library's 64 bits
     freqs = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.float32, device="cpu")  # whatever the default device is
     amplitude = ctypes.c_double()
     _check(lib().dfs_rope_frequencies(rot_dim, base, _SCALINGS[scaling], factor, original, beta_fast, beta_slow,

@@ -17,3 +17,10 @@ def test_frequencies_under_another_default_device(L, kw):  # noqa: F811
         away, _ = dfs.rope_frequencies(64, 10000.0, **kw, device="meta")
     assert got.device.type == "cpu" and torch.equal(got, want) and same == amplitude
     assert torch.equal(moved, want) and away.device.type == "meta" and away.shape == want.shape
+
+
+@pytest.mark.parametrize("rot", [1026, 1 << 40, 1 << 64, (1 << 64) + 64, 64 - (1 << 64), -(1 << 63), -64])
+def test_frequencies_of_sizes_that_no_head_has(L, rot):  # noqa: F811
+    """Refused as such, also what 64 bits do not hold, before anything is allocated or written for it."""
+    with pytest.raises(dfs.DfsError, match="DFS_E_SHAPE"):
+        dfs.rope_frequencies(rot)
