@@ -916,7 +916,7 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None,
     if freqs.dim() != 1:
         raise ValueError("freqs must be [rot_dim / 2]")
     s, rows, _, _ = _rope_shape(None if q is None else (q.shape, q.stride()), None if k is None else (k.shape, k.stride()),
-                                None if v is None else (v.shape, v.stride()), 2 * freqs.shape[0], layout, amplitude, dt)
+                                None if v is None else (v.shape, v.stride()), 2 * freqs.shape[0], layout, float(amplitude), dt)
     if positions.numel() != rows:
         raise ValueError(f"positions must be one for each of {rows} tokens")
     if out is None:
@@ -965,7 +965,7 @@ def cache_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, start
     if freqs is not None and freqs.dim() != 1:
         raise ValueError("freqs must be [rot_dim / 2]")
     s, _, Hkv, D = _rope_shape(None if q is None else (q.shape, q.stride()), (k.shape, k.stride()), (v.shape, v.stride()),
-                               0 if freqs is None else 2 * freqs.shape[0], layout, amplitude, dt)
+                               0 if freqs is None else 2 * freqs.shape[0], layout, float(amplitude), dt)
     pages, table, batch = k_pages.shape, block_table.shape, lens.shape
     if len(pages) != 4 or v_pages.shape != pages or pages[1] != Hkv or pages[3] != D:
         raise ValueError(f"k_pages and v_pages must both be [n_pages, {Hkv}, page_size, {D}]")

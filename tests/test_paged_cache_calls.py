@@ -24,3 +24,21 @@ def test_frequencies_of_sizes_that_no_head_has(L, rot):  # noqa: F811
     """Refused as such, also what 64 bits do not hold, before anything is allocated or written for it."""
     with pytest.raises(dfs.DfsError, match="DFS_E_SHAPE"):
         dfs.rope_frequencies(rot)
+
+
+def test_an_amplitude_is_taken_by_its_value(L, monkeypatch):  # noqa: F811
+    """One that is a tensor may change between two calls of the same sizes."""
+    seen = []
+    tensor = lambda t, *_: isinstance(t, torch.Tensor)  # noqa: E731
+    monkeypatch.setattr(dfs, "_fits", tensor)
+    monkeypatch.setattr(dfs, "_on", tensor)
+    monkeypatch.setattr(dfs, "_call", lambda index, where, fn, *args: seen.extend(a._obj.amplitude for a in args
+                                                                                if isinstance(getattr(a, "_obj", None), dfs._RopeShape)))
+    x, i, f = torch.zeros(2, 3, 64), torch.zeros(2, dtype=torch.int32), torch.ones(32)
+    pages, table, lens = torch.zeros(4, 3, 16, 64), torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    amplitude = torch.tensor(1.25)
+    for value in (1.25, 2.5):
+        amplitude.fill_(value)
+        dfs.rope(x, None, None, i, f, amplitude=amplitude)
+        dfs.cache_append(None, x, x, i, f, pages, pages.clone(), table, lens, amplitude=amplitude)
+    assert seen == [1.25, 1.25, 2.5, 2.5]
