@@ -411,8 +411,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, int block, Shared<C>& 
     // Smaller ones: the pages of step i's keys, into its slot of this wave's ring.
     auto look_up = [&](int i) {
       const int key = min((first + i) * C::kTile + kw * C::kKeys + (lane & (C::kKeys - 1)), len - 1);
-      const bool of_front = kRole == kBoth && key < front;
-      dma4((of_front ? a.prefix_table : table) + (max(of_front ? key : key - front, 0) >> a.c.page_shift),
+      dma4(kRole == kBoth ? page_entry(a.prefix_table, table, front, key, a.c.page_shift) : table + (max(key, 0) >> a.c.page_shift),
            __builtin_amdgcn_readfirstlane(pages0 + i % (C::kAhead + 1) * C::kPages));
     };
     // This wave's share of step i's K and V rows.

@@ -6,6 +6,15 @@
 
 namespace dfs {
 
+// The entry of a table that holds the page of key `key`, where the prefix's `front` keys lie in front of a sequence's own:
+// the prefix's or the sequence's.  Key -1: there are none at all, and what stands in for the sequence's table is read.
+__host__ __device__ __forceinline__ const int32_t* page_entry(const int32_t* prefix_table, const int32_t* table,
+                                                              int front, int key, int page_shift) {
+  const bool of_front = key >= 0 && key < front;
+  const int at = of_front ? key : key - front;
+  return (of_front ? prefix_table : table) + ((at > 0 ? at : 0) >> page_shift);
+}
+
 // Row tiles x key tiles of a kv head over its C workgroups, as evenly as it goes with few pieces.  First whole row
 // tiles, a workgroup each and C at a time; the n < C that are left, with f = C / n workgroups each and e = C % n over:
 // workgroup (tile, c) takes `each` key tiles from c * each on, and the e others share what lies behind f * each of
