@@ -841,11 +841,14 @@ static int check_rope_shape(const dfs_rope_shape_t* s, bool q, bool k, bool v, i
   return DFS_OK;
 }
 
-// The bytes that an input of `heads` heads spans, and that its dense rows have.
+// The bytes that an input of `heads` heads spans, and that its dense rows have.  Sizes of what is not given may be
+// anything.
 static Span strided(const void* p, const dfs_rope_shape_t& s, int64_t stride, int64_t heads) {
+  if (!p) return {nullptr, 0};
   return {p, (size_t)((s.rows - 1) * stride + heads * s.head_dim) * esize(s.dtype)};
 }
 static Span dense(const void* p, const dfs_rope_shape_t& s, int64_t heads) {
+  if (!p) return {nullptr, 0};
   return {p, (size_t)(s.rows * heads * s.head_dim) * esize(s.dtype)};
 }
 
@@ -876,7 +879,8 @@ int dfs_rope(const void* q, const void* k, const void* v, const int32_t* positio
                       strided(v, s, s.v_stride, s.kv_heads), {positions, (size_t)s.rows * 4},
                       {freqs, (size_t)s.rot_dim * 2}};
   const Span out[3] = {dense(out_q, s, s.q_heads), dense(out_k, s, s.kv_heads), dense(out_v, s, s.kv_heads)};
-  const int place[3] = {s.q_stride == s.q_heads * s.head_dim ? 0 : -1, s.k_stride == s.kv_heads * s.head_dim ? 1 : -1, -1};
+  const int place[3] = {q && s.q_stride == s.q_heads * s.head_dim ? 0 : -1,
+                        k && s.k_stride == s.kv_heads * s.head_dim ? 1 : -1, -1};
   if (any_overlap(in, out, place)) return DFS_E_ARG;
   if ((st = check_device()) != DFS_OK) return st;
   (void)hipGetLastError();
@@ -907,7 +911,7 @@ int dfs_cache_append(const void* q, const void* k, const void* v, const int32_t*
                       {r.rot_dim > 0 ? freqs : nullptr, (size_t)r.rot_dim * 2}, {prefix_len, 4},
                       {block_table, (size_t)(s.batch * s.table_width) * 4}, {lens, bn}};
   const Span out[4] = {dense(out_q, r, r.q_heads), {k_pages, pn}, {v_pages, pn}, {out_lens, bn}};
-  if (any_overlap(in, out, {r.q_stride == r.q_heads * r.head_dim ? 0 : -1, -1, -1, -1})) return DFS_E_ARG;
+  if (any_overlap(in, out, {q && r.q_stride == r.q_heads * r.head_dim ? 0 : -1, -1, -1, -1})) return DFS_E_ARG;
   if ((st = check_device()) != DFS_OK) return st;
   (void)hipGetLastError();
   return hip_status(launch_cache_append(rope_job(r, q, k, v, freqs, out_q, nullptr, nullptr),

@@ -1,10 +1,13 @@
 """Calls of the operators around a paged cache that differ from the usual ones in what surrounds them (CPU)."""
+import ctypes
+
 import pytest
 import torch
 
 import draft_selection_position_amd as dfs
 
-from .test_target_pass_oracle import L  # noqa: F401
+from .test_paged_cache_oracle import _rope
+from .test_target_pass_oracle import FAR, L, P, _shape, passes  # noqa: F401
 
 
 @pytest.mark.parametrize("kw", [dict(), dict(scaling="yarn", factor=8.0, original=4096.0)])
@@ -42,3 +45,24 @@ def test_an_amplitude_is_taken_by_its_value(L, monkeypatch):  # noqa: F811
         dfs.rope(x, None, None, i, f, amplitude=amplitude)
         dfs.cache_append(None, x, x, i, f, pages, pages.clone(), table, lens, amplitude=amplitude)
     assert seen == [1.25, 1.25, 2.5, 2.5]
+
+
+@pytest.mark.parametrize("any_", [2 ** 63 - 1, -2 ** 63, 2 ** 62 + 8, -1, 0])
+def test_sizes_that_are_not_looked_at(L, any_):  # noqa: F811
+    """Those of heads that are not given, the rows' strides of them, and what the append does without."""
+    heads = dict(q=dict(q_heads=any_, q_stride=any_), kv=dict(kv_heads=any_, k_stride=any_, v_stride=any_))
+
+    def rope(kw, q, k, v):
+        ins, outs = ([P + (i << 36) if there else None for i, there in enumerate((q, k, v))],
+                     [FAR + (i << 36) if there else None for i, there in enumerate((q, k, v))])
+        return L.dfs_rope(*ins, P + (4 << 36), P + (5 << 36), ctypes.byref(_rope(**kw)), *outs, None)
+
+    assert passes(rope, heads["q"], False, True, True) and passes(rope, heads["kv"], True, False, False)
+    assert passes(rope, dict(k_stride=any_), True, False, True) and passes(rope, dict(v_stride=any_), True, True, False)
+
+    def append(rope_kw, shape_kw):
+        a = [P + (i << 36) for i in range(9)]
+        return L.dfs_cache_append(None, a[0], a[1], a[2], a[3], ctypes.byref(_rope(**rope_kw)), a[4], None, a[5], a[6], a[7], a[8],
+                                  ctypes.byref(_shape(**shape_kw)), FAR, None)
+
+    assert passes(append, heads["q"], dict(T=any_, q_heads=any_))
