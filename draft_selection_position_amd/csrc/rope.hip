@@ -7,8 +7,9 @@
 // one token, computes the token's angles once, a lane each, into LDS, and every lane keeps the
 // sines and cosines of the pairs that it has in all of its heads.
 //
-// Angles.  a / (pi / 2) = n + r, |r| <= 1/2, formed in 64 bits (two roundings: at position 2^20 and
-// frequency 1 the quarter turn is off by 2^-32).  Sine and cosine of r pi / 2 are their series in fp32
+// Angles.  a / (pi / 2) = n + r, |r| <= 1/2, in 64 bits with what the products' roundings lose carried along: position times
+// frequency has up to 56 bits, and its last ones are worth 2^-21 of a turn's quarter at position 2^32 and frequency 1.  So r is
+// off by 2^-53 wherever n is exact, n < 2^53; beyond that an angle has no digits left.  Sine and cosine of r pi / 2 are their series in fp32
 // (the terms left out are below 2^-29 and 2^-33); n picks the quadrant.
 //
 // Bound by memory: 16320 tokens of 32 + 8 heads of 128, k and v out of their joint rows too, bf16, 401 MB read and written: 78.5 us, 5.1
@@ -45,10 +46,14 @@ struct Args {
 
 // cos and sin of pos f, times the amplitude.
 __device__ __forceinline__ float2 turn_of(int64_t pos, float f, float amplitude) {
-  const double quarters = (double)pos * ((double)f * 0.63661977236758134308);  // 2 / pi
-  const double n = rint(quarters);
-  const float x = (float)(quarters - n) * 1.57079632679489661923f;
-  const int k = (int)(int64_t)n & 3;
+  constexpr double kHigh = 0.63661977236758134308, kLow = -3.9357353350364971764e-17;  // 2 / pi
+  const double p = (double)pos, angle = p * (double)f;
+  const double n = rint(angle * kHigh);
+  double r = fma(angle, kHigh, -n) + fma(angle, kLow, fma(p, (double)f, -angle) * kHigh);
+  const double m = rint(r);  // a border's other side; all that is left of an angle past 2^53
+  r -= m;
+  const float x = (float)r * 1.57079632679489661923f;
+  const int k = (int)(((int64_t)n & 3) + ((int64_t)m & 3)) & 3;
   const float z = x * x;
   float s = fmaf(z, 2.75573192e-6f, -1.98412698e-4f);  // 1/9!, 1/7!, 1/5!, 1/3!
   s = fmaf(s, z, 8.33333333e-3f);

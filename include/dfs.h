@@ -450,8 +450,8 @@ int dfs_tree_positions(const int32_t* parents, const int32_t* lens, const int32_
  *   (x1, x2) -> A (x1 cos a - x2 sin a,  x2 cos a + x1 sin a),   a = position freqs[i]
  *   DFS_ROPE_HALF: pair i is (x[i], x[i + rot_dim / 2]); DFS_ROPE_INTERLEAVED: (x[2 i], x[2 i + 1])
  * The rest of a head is copied (A does not apply to it).  The angle's product and its reduction
- * are taken in 64 bits, so that far positions lose nothing; sine, cosine and the turn in fp32,
- * rounded once. */
+ * are taken in 64 bits with their rounding errors carried along, so that far positions lose nothing
+ * (of angles below 2^53; larger ones turn by some angle); sine, cosine and the turn in fp32, rounded once. */
 typedef enum DFS_ENUM_BASE { DFS_ROPE_HALF = 0, DFS_ROPE_INTERLEAVED = 1 } dfs_rope_layout_t;
 typedef struct {
   int64_t rows;      /* tokens, 1..DFS_MAX_ROWS */
