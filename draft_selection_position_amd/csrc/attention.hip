@@ -32,7 +32,8 @@
 //
 // A batch with a shared prefix takes the same steps over two sets of keys: the prefix's, with the rows of the whole
 // batch as those of one sequence (by the kernel here, or for many by one of its own: prefix.hip), and every
-// sequence's own.  Both leave pieces, and the join takes a row's of either kind.  4 tokens, 8 kv heads x 4 of 128, 4001 + up to
+// sequence's own.  Both leave pieces, and the join takes a row's of either kind; only where there are few keys in all does
+// every sequence take the prefix's as if they were its own, in one launch without pieces.  4 tokens, 8 kv heads x 4 of 128, 4001 + up to
 // 77 keys: 14.3 us, two launches as above; 256 tokens, 16384 + up to 1024 keys: 187 to 207 us, of which 78 the prefix,
 // 102 the own keys (5.2 TB/s) and 10 the join; each by itself (no prefix known) would read 17.2 GB.
 #include <algorithm>
@@ -817,9 +818,13 @@ auto with_cfg(int64_t rows, F f) {
 // How a batch goes over its shared prefix.  Few rows or few products: tree attention's kernel, in one launch with the
 // sequences' own keys, so that the call is two launches.  From 3 x 2^32 products of a kind on (rows x heads x the
 // prefix's longest x D), and more than 384 rows: the prefix's own kernel, which is half as fast again but fills
-// slowly and takes tiles of 256 rows (us, own kernel against the other: 512 rows x 8 heads of 128 x 32768 keys 99 and 106, 4352 x
-// 8 x 8000 190 and 238, 4352 x 8 of 64 x 8000 113 and 158; below, 768 x 8 x 16384 94 and 98, 1020 x 4 x 16384 83 and 66,
-// 544 x 8 x 1000 44 and 28; 384 x 8 x 65536 179 and 171).
+// slowly and takes tiles of 256 rows (us, own kernel against the other: heads of 128, 512 rows x 8 heads x 32768 keys 99 and 106, 4352 x 8 x
+// 8000 167 and 230, 4536 x 4 x 8000 105 and 124; below, 2176 x 4 x 8000 70 and 65, 4352 x 8 x 2000 80 and 77, 768 x 8 x 16384 94 and 98, 1020 x
+// 4 x 16384 83 and 66, 544 x 8 x 1000 44 and 28, 384 x 8 x 65536 179 and 171.  Heads of 64, 4352 x 8 x 8000 112 and 158, 4352 x 4 x 16000 114
+// and 141, 17227 x 4 x 4000 136 and 201; below, 4352 x 8 x 2000 61 and 55, 4352 x 4 x 8000 81 and 78, 4536 x 4 x 8000 81 and 65).
+// Products are not all that decides, for row tiles fill the card's workgroups well or badly: below the bound the own kernel gains at 4352 x 4 of 128
+// x 4000 (78 and 126) and x 2000 (60 and 74), 6426 x 4 of 128 x 2000 (76 and 79), 17227 x 4 of 128 x 900 (103 and 113), of 64 x 2000 (103 and 115),
+// 4352 x 8 of 64 x 4000 (84 and 89), and above it loses at 6426 x 4 of 64 x 8000 (107 and 89), 4536 x 4 of 64 x 16000 (118 and 112).
 bool prefix_is_large(int64_t rows, int64_t kv_heads, int64_t D, int64_t longest) {
   return rows > 384 && (double)rows * (double)kv_heads * (double)D * (double)longest >= 3.0 * 4294967296.0;
 }
@@ -840,8 +845,12 @@ bool own_by_waves(int64_t rows, int64_t pairs, int64_t longest) { return rows <=
 // Few keys in all, by the tables' widths: a workgroup takes the prefix's and a sequence's own, in one launch and without
 // pieces, although every sequence reads the prefix again (us, against the other ways; heads of 128, 4 to each of 8 kv heads: 64 x 17
 // nodes, prefix 100, up to 50 own keys 20 and 35, 550 and 50 35 and 44, 900 and 50 49 and 50; 32 tokens, 300 and 100 14 and 18, 4
-// tokens 14.0 and 13.1 but a launch less for the host, 8 tokens, 900 and 50 20 and 13; 256 tokens, 100 and 100 70 and 44; 183 x 26 nodes, 7
-// x 2, 2 and 65 40 and 62; 107 x 23, 4 x 7 of 64, 600 43 and 56).
+// tokens 13.0 and 12.5 but a launch less for the host, 8 tokens, 900 and 50 20 and 13; 183 x 26 nodes, 7 x 2, 2 and 65 40 and 62; 107 x 23, 4
+// x 7 of 64, 600 43 and 56).  Up to 32 rows a CU holds one workgroup, so that a 257th begins when another ends: 32 tokens x 8 heads of 128, 300
+// and 100 13.7 and 18.1, 33 22.4 and 18.3, 48 24.3 and 19.2, 64 25.6 and 24.8, 96 (not taken) 37 and 27; with 6 nodes 36 26.4 and 23.8, 48 27.3
+// and 28.1, 64 28.6 and 29.4; of 64, 33 15.6 and 14.3, 64 16.7 and 17.4, with 6 nodes 33 16.6 and 21.6, 64 18.5 and 24.4: between 256
+// and 512 pairs few rows lose and more rows gain.  Beyond 32 rows any number of pairs gains: 8 x 17 nodes x 8 heads, 128 and 40 13.5 and 16.2, 256 x
+// 17 x 8 64 and 98, 1024 x 17 x 4 123 and 247, 550 and 60 251 and 348; at worst 600 x 40 nodes x 4 heads, 550 and 60 148 and 144.
 bool few_keys(int64_t rows, int64_t pairs, int64_t longest) {
   if (rows <= 32) return longest <= 512 && pairs <= 512;
   return longest <= 256 || (longest <= 768 && pairs * cdiv(rows, 128) >= 48);

@@ -12,11 +12,17 @@
 // one only with another of its own.  So pages are looked up by scalar loads, addresses are scalar sums, loads past
 // the end fetch the last stage again, and the one branch (a maximum that lags, or the prefix's end) is out of the way.
 //
-// What bounds it (MI355X; cycles of a half's 32 x 32 scores, 512 of matrix cores at head 128): 890, of which 710
-// are matrix and vector instructions as a wave alone issues them, 80 loads into LDS, 65 the barrier, 65 LDS reads.  64 x
-// 17 rows x 4 heads of 128 for each of 8 kv heads, 16384 keys: 281 to 300 us, 1000 TFLOP/s at 1.9 GHz (32 rows a wave,
-// two waves a SIMD: 480).  Head 64 is bound by the vector unit (440 cycles of 256): 12 x 63 x 6 rows for 4 kv
-// heads, 60001 keys, 320 to 350 us, 830 TFLOP/s (480 to 500).
+// Weights are rounded to bf16 for the second product, 2^-8 of each at most, as in tree attention, and the sums take them as they
+// were: the roundings of a sum's many weights cancel (2-norm errors 0.00228 with either kind of sum; 0.0016 with weights
+// in fp32, which is the output's own rounding).
+//
+// What bounds it (MI355X; cycles of a SIMD for a half's 32 x 32 scores, 512 of matrix cores at head 128): 890 in the loop, of which 710
+// are matrix and vector instructions as a wave alone issues them, 80 loads into LDS, 65 the barrier, 65 LDS reads; 1010 with
+// the starts and ends of the ranges.  64 x 17 rows x 4 heads of 128 for each of 8 kv heads, 16384 keys: 281 to 308 us (up to 331 from a cold
+// start), 950 to 1040 TFLOP/s at 1.9 to 2.0 GHz (32 rows a wave, two waves a SIMD: 480).
+// Head 64: 540 in all, 256 of matrix cores.  What the two waves issue nearly fills it: 426 of vector instructions (89, of which 16
+// exponentials at 8 cycles), 107 of scalar ones, 24 of LDS reads; a wave waits for its turn to issue for a third of its time, for memory
+// or the barrier for a tenth.  12 x 63 x 6 rows for 4 kv heads, 60001 keys: 320 to 350 us, 830 TFLOP/s (480 to 500).
 #include <algorithm>
 #include <type_traits>
 
